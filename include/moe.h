@@ -44,6 +44,8 @@
  *   - Device-side problems (an expert id >= E or < -1, a bounded wait that ran
  *     out) are recorded in an error word inside the workspace; read it with
  *     moe_check_device_error().  A slot with such an id is not routed either.
+ *   - The row operators and the MXFP4 operators (moe_permute ... moe_mxfp4_gemm)
+ *     work on the caller's own tensors and need no plan.
  *   - Every call is asynchronous on `stream` (a cudaStream_t; NULL = legacy
  *     default stream) unless stated otherwise.  Calls with different plans or
  *     different workspaces may run concurrently; two calls sharing one
@@ -275,6 +277,140 @@ moe_status moe_combine(moe_plan_t plan, const float *topk_w, void *out,
  * x_bf16 16-byte and x_codes 8-byte aligned.  Needs no plan or workspace.   */
 moe_status moe_quantize_act(const void *x_bf16, int T, int H, uint8_t *x_codes,
                             uint8_t *x_scales, moe_stream_t stream);
+
+/* ---- Row operators: tokens in expert order and back, without a plan. --------
+ * They take the routing that moe_route() or moe_route_static() computes: inv
+ * i32[T*k], the position of slot t*k + j in expert order, each position used
+ * once, -1 for a slot that is not routed.  A position outside [0, T*k) is
+ * treated as -1.  (If two slots name one position, the row written there is one
+ * of the two.)  Rows are S = T*k rows of H elements in expert order; rows that no slot names --
+ * behind the last routed one -- are neither read nor written.  Sums run in
+ * fp32, j ascending, and are rounded once to the row type; no atomics, so
+ * results repeat bitwise.  An output may not overlap an input
+ * (MOE_ERR_INVALID_ARG).  All calls are one launch on `stream`, can be captured
+ * into a graph, and may run concurrently with one another.
+ * T >= 1, k >= 1 (k may exceed the layer's 256 experts), T*k < 2^31; rows of a
+ * multiple of 16 bytes (MOE_ERR_UNSUPPORTED otherwise).                      */
+typedef enum { MOE_T_BF16 = 0, MOE_T_FP16 = 1, MOE_T_FP32 = 2 } moe_dtype;
+
+/* rows[inv[t*k + j]] = x[t] for every routed slot; a copy of bytes, so any
+ * element type: row_bytes is the length of a row (x [T, row_bytes], rows
+ * [T*k, row_bytes]), here a multiple of 4 (16-byte multiples copy fastest).
+ * Source: DeepGEMM PR #386 Description (tokens grouped per expert).         */
+moe_status moe_permute(const void *x, int T, int64_t row_bytes, int k, const int32_t *inv,
+                       void *rows, moe_stream_t stream);
+
+/* The gradient of moe_permute: dx[t] = sum_j drows[inv[t*k + j]] over the
+ * routed slots (0 for a token without any).  drows [T*k, H], dx [T, H], both of
+ * `dtype` (a moe_dtype).
+ * No counterpart on the pages.
+ */
+moe_status moe_permute_backward(const void *drows, int dtype, int T, int H, int k,
+                                const int32_t *inv, void *dx, moe_stream_t stream);
+
+/* out[t] = sum_j topk_w[t*k + j] * rows[inv[t*k + j]] over the routed slots (0
+ * for a token without any; the weight of a slot that is not routed is not
+ * used).  rows [T*k, H], out [T, H] of `dtype`, topk_w f32 [T, k].
+ * Source: DeepGEMM PR #386 title ("direct combine").
+ */
+moe_status moe_unpermute(const void *rows, int dtype, int T, int H, int k, const int32_t *inv,
+                         const float *topk_w, void *out, moe_stream_t stream);
+
+/* The gradients of moe_unpermute, from dout [T, H]:
+ *   drows[inv[t*k + j]] = topk_w[t*k + j] * dout[t]       [T*k, H] of `dtype`
+ *   dw[t*k + j]         = <dout[t], rows[inv[t*k + j]]>   f32 [T, k], written
+ *                         entirely (0 for a slot that is not routed)
+ * Either drows or dw may be NULL (that gradient is not wanted); rows may be
+ * NULL when dw is.
+ * No counterpart on the pages.
+ */
+moe_status moe_unpermute_backward(const void *dout, const void *rows, int dtype, int T, int H,
+                                  int k, const int32_t *inv, const float *topk_w, void *drows,
+                                  float *dw, moe_stream_t stream);
+
+/* ---- MXFP4: E2M1 codes with one UE8M0 scale per 32 elements of a row. -------
+ * Codes are u8 [R, K/2], element 2i in the low nibble of byte i; K % 32 == 0.
+ * Scale bytes come in one of two layouts:
+ *   MOE_SCALES_ROW_MAJOR    u8 [R, K/32], the layout of the layer's MXFP4 weights
+ *   MOE_SCALES_GROUP_MAJOR  u8 [ceil(K/128), R, 4]: byte (g, r, j) scales row r's
+ *                           elements 128g + 32j .. + 31 (0 past K); the layout
+ *                           moe_mxfp4_gemm takes for its rows               */
+typedef enum { MOE_SCALES_ROW_MAJOR = 0, MOE_SCALES_GROUP_MAJOR = 1 } moe_scale_layout;
+
+/* Quantise x [T, K] of `dtype`.  Per 32 elements: n = the smallest integer
+ * >= -127 with amax <= 6 * 2^n, scale byte n + 127, codes = E2M1 of x / 2^n,
+ * round to nearest even.  (Unlike moe_quantize_act there is no floor under
+ * amax: E2M1 spans a factor of 12, so a floor would flush small blocks.)  A
+ * block with a NaN or an infinity gets scale byte 255 (NaN) and codes 0.
+ * With inv (as for the row operators) the T tokens' rows are written once per
+ * routed slot, straight into expert order: codes and scales have R = T*k rows,
+ * and rows that no slot names are left as they were.  inv NULL (then k must be
+ * 1): R = T, in order.  x and codes 16-byte, scales 4-byte aligned.
+ * Source: the MXFP4 weights of the FP8/FP4 variant (fw-ai/DeepGEMM PR #16,
+ * Overview); the pages show no quantiser for them.
+ */
+moe_status moe_quantize_mxfp4(const void *x, int dtype, int T, int K, int k, const int32_t *inv,
+                              uint8_t *codes, uint8_t *scales, int scale_layout,
+                              moe_stream_t stream);
+
+/* out[r, c] = E2M1 code * 2^(scale byte - 127), out [R, K] of `dtype`: exact in
+ * bf16 and fp32 below 2^128 and infinity from there on (fp16 rounds to nearest,
+ * to infinity past its range); NaN for scale byte 255.
+ * No counterpart on the pages.
+ */
+moe_status moe_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, int scale_layout,
+                                int R, int K, int dtype, void *out, moe_stream_t stream);
+
+/* Bytes of moe_mxfp4_prepack's two outputs; 0 for sizes that moe_mxfp4_gemm does
+ * not take (1 <= E <= 256, N % 8 == 0, K % 32 == 0, N and K at most 2^20).
+ * No counterpart on the pages.
+ */
+size_t moe_mxfp4_weight_bytes(int E, int N, int K);
+size_t moe_mxfp4_weight_scale_bytes(int E, int N, int K);
+
+/* Lay out MXFP4 weights for moe_mxfp4_gemm, once per weight set: w u8 [E, N,
+ * K/2] and w_scales u8 [E, N, K/32] row-major -> tiles of 128 rows x 256 codes,
+ * 16 KB each, swizzled as the tensor core reads them, and the scale chunks that
+ * go with them (N and K are filled up with zeros to whole tiles).  Buffers
+ * 16-byte aligned, not overlapping.  Enqueued on `stream`.
+ * No counterpart on the pages (a storage layout for this library's tensor-
+ * core kernels).
+ */
+moe_status moe_mxfp4_prepack(const uint8_t *w, const uint8_t *w_scales, int E, int N, int K,
+                             uint8_t *w_tiled, uint8_t *w_scales_chunked, moe_stream_t stream);
+
+/* Bytes of moe_mxfp4_gemm's workspace (device, 256-byte aligned); 0 for sizes it
+ * does not take.  Zero the workspace once before its first use; calls leave it
+ * ready for the next.  Calls that may overlap on the GPU need workspaces of
+ * their own.
+ * No counterpart on the pages.
+ */
+size_t moe_mxfp4_workspace_bytes(int R, int E, int N, int K);
+
+/* Grouped product of MXFP4 rows with MXFP4 weights, on the tensor cores with
+ * both scales applied in hardware:
+ *   out[r, n] = sum_c a[r, c] * w[e, n, c]  for offsets[e] <= r < offsets[e+1]
+ * in fp32, rounded once to `dtype` (MOE_T_BF16 or MOE_T_FP16; MOE_T_FP32 is
+ * MOE_ERR_UNSUPPORTED).  codes u8 [R, K/2] and scales (group-major) are the rows
+ * in expert order; offsets i32 [E+1] on the device as moe_route() writes it
+ * (values are clamped to [0, R] and to be non-decreasing), or NULL for one group
+ * of all R rows (then E must be 1).  out [R, N]: rows outside every group are
+ * left as they were.  N % 8 == 0, K % 32 == 0, E <= 256.  A device-side wait that
+ * runs out is recorded in the workspace (moe_mxfp4_check_error).
+ * Source: the FP4 tensor-core path the pages name for SM100 (fw-ai/DeepGEMM PR
+ * #16, Overview).
+ */
+moe_status moe_mxfp4_gemm(const uint8_t *codes, const uint8_t *scales, const int32_t *offsets,
+                          int R, int E, int N, int K, const uint8_t *w_tiled,
+                          const uint8_t *w_scales_chunked, int dtype, void *out,
+                          void *workspace, moe_stream_t stream);
+
+/* Zero the workspace's error word (enqueued on `stream`), and read it: the
+ * latter synchronises `stream` and returns MOE_OK or MOE_ERR_DEVICE_TIMEOUT.
+ * No counterpart on the pages.
+ */
+moe_status moe_mxfp4_clear_error(void *workspace, moe_stream_t stream);
+moe_status moe_mxfp4_check_error(const void *workspace, moe_stream_t stream);
 
 /* Allocation-free routing.  The pages have no counterpart of this entry point.
  *

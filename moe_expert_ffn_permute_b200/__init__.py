@@ -22,6 +22,8 @@ STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED",
                 6: "MOE_ERR_BAD_ROUTING"}
 W_DTYPES = {"e4m3": 0, "e2m1": 1, "bf16": 2}
 ACT_KINDS = {"swiglu": 0, "swiglu_oai": 1}
+DTYPES = {"bf16": 0, "fp16": 1, "fp32": 2}            # moe_dtype
+SCALE_LAYOUTS = {"row": 0, "group": 1}                # moe_scale_layout
 
 
 class MoEError(RuntimeError):
@@ -48,6 +50,7 @@ class WorkspaceView(ctypes.Structure):
 
 
 _P = ctypes.c_void_p
+_I = ctypes.c_int
 _SIGS = {
     "moe_plan": (ctypes.c_int, [ctypes.c_int] * 5 + [_Dtypes, _Act, ctypes.POINTER(_P)]),
     "moe_plan_destroy": (None, [_P]),
@@ -81,6 +84,19 @@ _SIGS = {
     "moe_check_device_error": (ctypes.c_int, [_P] * 3),
     "moe_status_str": (ctypes.c_char_p, [ctypes.c_int]),
     "moe_forward_launch_count": (ctypes.c_int, [_P]),
+    "moe_permute": (ctypes.c_int, [_P, _I, ctypes.c_int64, _I, _P, _P, _P]),
+    "moe_permute_backward": (ctypes.c_int, [_P] + [_I] * 4 + [_P] * 3),
+    "moe_unpermute": (ctypes.c_int, [_P] + [_I] * 4 + [_P] * 4),
+    "moe_unpermute_backward": (ctypes.c_int, [_P] * 2 + [_I] * 4 + [_P] * 5),
+    "moe_quantize_mxfp4": (ctypes.c_int, [_P] + [_I] * 4 + [_P] * 3 + [_I, _P]),
+    "moe_dequantize_mxfp4": (ctypes.c_int, [_P] * 2 + [_I] * 4 + [_P] * 2),
+    "moe_mxfp4_weight_bytes": (ctypes.c_size_t, [_I] * 3),
+    "moe_mxfp4_weight_scale_bytes": (ctypes.c_size_t, [_I] * 3),
+    "moe_mxfp4_prepack": (ctypes.c_int, [_P] * 2 + [_I] * 3 + [_P] * 3),
+    "moe_mxfp4_workspace_bytes": (ctypes.c_size_t, [_I] * 4),
+    "moe_mxfp4_gemm": (ctypes.c_int, [_P] * 3 + [_I] * 4 + [_P] * 2 + [_I] + [_P] * 3),
+    "moe_mxfp4_clear_error": (ctypes.c_int, [_P] * 2),
+    "moe_mxfp4_check_error": (ctypes.c_int, [_P] * 2),
 }
 
 _lib = None
@@ -362,6 +378,194 @@ def moe_status_str(status):
 
 def moe_forward_launch_count(plan):
     return lib().moe_forward_launch_count(plan)
+
+
+def _sizes(fn, *values):
+    """C ints of a call: whole numbers that fit, so that none wraps around."""
+    for v in values:
+        if not -(1 << 31) <= v < (1 << 31):
+            raise MoEError(MOE_ERR_INVALID_ARG, f"{fn}: {v} does not fit a C int")
+
+
+def _choice(fn, name, table, value):
+    try:
+        return table[value]
+    except (KeyError, TypeError):
+        raise MoEError(MOE_ERR_INVALID_ARG,
+                       f"{fn}: {name} must be one of {', '.join(table)}, got {value!r}") from None
+
+
+def _buffers(fn, *args):
+    """Addresses of a call's buffers, given as (name, tensor or address or None,
+    bytes the call reads or writes, torch dtype names it may have).  The C ABI
+    sees only pointers, so a tensor is checked here: contiguous, on the current
+    device, of the right type and long enough.  A raw address is passed through
+    (the caller vouches for it), and so is None (the library refuses it where it
+    is required)."""
+    device = None
+    out = []
+    for name, t, nbytes, dtypes in args:
+        if t is None or isinstance(t, int):
+            out.append(t)
+            continue
+        at = t.get_device()
+        if device is None:
+            import torch
+            device = torch.cuda.current_device() if at >= 0 else -2
+        if at != device:
+            raise MoEError(MOE_ERR_INVALID_ARG, f"{fn}: {name} must be on the current CUDA device, "
+                                                f"is on {t.device}")
+        if not t.is_contiguous():
+            raise MoEError(MOE_ERR_INVALID_ARG, f"{fn}: {name} must be contiguous")
+        if dtypes is not None and str(t.dtype)[6:] not in dtypes:
+            raise MoEError(MOE_ERR_INVALID_ARG,
+                           f"{fn}: {name} must be {' or '.join(dtypes)}, got {t.dtype}")
+        if t.numel() * t.element_size() < nbytes:
+            raise MoEError(MOE_ERR_INVALID_ARG,
+                           f"{fn}: {name} holds {t.numel() * t.element_size()} bytes, needs {nbytes}")
+        out.append(t.data_ptr())
+    return out
+
+
+_I32, _F32, _U8 = ("int32",), ("float32",), ("uint8",)
+_ELEM = {"bf16": (2, ("bfloat16",)), "fp16": (2, ("float16",)), "fp32": (4, ("float32",))}
+
+
+def moe_permute(x, T, row_bytes, k, inv, rows, stream=None):
+    """rows[inv[t, j]] = x[t]: x [T, row_bytes] of any type -> rows [T*k, row_bytes]."""
+    _sizes("moe_permute", T, k)
+    x, inv, rows = _buffers("moe_permute", ("x", x, T * row_bytes, None), ("inv", inv, 4 * T * k, _I32),
+                            ("rows", rows, T * k * row_bytes, None))
+    _check(lib().moe_permute(x, T, row_bytes, k, inv, rows, _stream(stream)), "moe_permute")
+
+
+def moe_permute_backward(drows, dtype, T, H, k, inv, dx, stream=None):
+    """dx[t] = sum_j drows[inv[t, j]]; dtype "bf16", "fp16" or "fp32"."""
+    d = _choice("moe_permute_backward", "dtype", DTYPES, dtype)
+    _sizes("moe_permute_backward", T, H, k)
+    z, tt = _ELEM[dtype]
+    drows, inv, dx = _buffers("moe_permute_backward", ("drows", drows, T * k * H * z, tt),
+                              ("inv", inv, 4 * T * k, _I32), ("dx", dx, T * H * z, tt))
+    _check(lib().moe_permute_backward(drows, d, T, H, k, inv, dx, _stream(stream)),
+           "moe_permute_backward")
+
+
+def moe_unpermute(rows, dtype, T, H, k, inv, topk_w, out, stream=None):
+    """out[t] = sum_j topk_w[t, j] * rows[inv[t, j]]; dtype "bf16", "fp16" or "fp32"."""
+    d = _choice("moe_unpermute", "dtype", DTYPES, dtype)
+    _sizes("moe_unpermute", T, H, k)
+    z, tt = _ELEM[dtype]
+    rows, inv, topk_w, out = _buffers(
+        "moe_unpermute", ("rows", rows, T * k * H * z, tt), ("inv", inv, 4 * T * k, _I32),
+        ("topk_w", topk_w, 4 * T * k, _F32), ("out", out, T * H * z, tt))
+    _check(lib().moe_unpermute(rows, d, T, H, k, inv, topk_w, out, _stream(stream)),
+           "moe_unpermute")
+
+
+def moe_unpermute_backward(dout, rows, dtype, T, H, k, inv, topk_w, drows, dw, stream=None):
+    """drows[inv[t, j]] = topk_w[t, j] * dout[t]; dw[t, j] = <dout[t], rows[inv[t, j]]>.
+    drows or dw may be None; rows too when dw is."""
+    d = _choice("moe_unpermute_backward", "dtype", DTYPES, dtype)
+    _sizes("moe_unpermute_backward", T, H, k)
+    z, tt = _ELEM[dtype]
+    args = _buffers("moe_unpermute_backward", ("dout", dout, T * H * z, tt),
+                    ("rows", rows, T * k * H * z, tt), ("inv", inv, 4 * T * k, _I32),
+                    ("topk_w", topk_w, 4 * T * k, _F32), ("drows", drows, T * k * H * z, tt),
+                    ("dw", dw, 4 * T * k, _F32))
+    _check(lib().moe_unpermute_backward(args[0], args[1], d, T, H, k, *args[2:], _stream(stream)),
+           "moe_unpermute_backward")
+
+
+def mxfp4_scale_shape(R, K, layout):
+    """Shape of the scale bytes of R rows of K elements, layout "row" or "group"."""
+    return (R, K // 32) if layout == "row" else ((K + 127) // 128, R, 4)
+
+
+def moe_quantize_mxfp4(x, dtype, T, K, k, inv, codes, scales, scale_layout="row", stream=None):
+    """x [T, K] -> E2M1 codes u8 [T*k, K/2] and UE8M0 scales (mxfp4_scale_shape), each
+    token's row at the positions of its slots; inv None (k = 1): in order."""
+    d = _choice("moe_quantize_mxfp4", "dtype", DTYPES, dtype)
+    s = _choice("moe_quantize_mxfp4", "scale_layout", SCALE_LAYOUTS, scale_layout)
+    _sizes("moe_quantize_mxfp4", T, K, k)
+    z, tt = _ELEM[dtype]
+    R = T * k
+    nscale = R * (K // 32) if s == 0 else (K + 127) // 128 * R * 4
+    x, inv, codes, scales = _buffers(
+        "moe_quantize_mxfp4", ("x", x, T * K * z, tt), ("inv", inv, 4 * R, _I32),
+        ("codes", codes, R * (K // 2), _U8), ("scales", scales, nscale, _U8))
+    _check(lib().moe_quantize_mxfp4(x, d, T, K, k, inv, codes, scales, s, _stream(stream)),
+           "moe_quantize_mxfp4")
+
+
+def moe_dequantize_mxfp4(codes, scales, scale_layout, R, K, dtype, out, stream=None):
+    """The values of codes u8 [R, K/2] and their scales -> out [R, K]."""
+    d = _choice("moe_dequantize_mxfp4", "dtype", DTYPES, dtype)
+    s = _choice("moe_dequantize_mxfp4", "scale_layout", SCALE_LAYOUTS, scale_layout)
+    _sizes("moe_dequantize_mxfp4", R, K)
+    z, tt = _ELEM[dtype]
+    nscale = R * (K // 32) if s == 0 else (K + 127) // 128 * R * 4
+    codes, scales, out = _buffers(
+        "moe_dequantize_mxfp4", ("codes", codes, R * (K // 2), _U8), ("scales", scales, nscale, _U8),
+        ("out", out, R * K * z, tt))
+    _check(lib().moe_dequantize_mxfp4(codes, scales, s, R, K, d, out, _stream(stream)),
+           "moe_dequantize_mxfp4")
+
+
+def moe_mxfp4_weight_bytes(E, N, K):
+    """Bytes of prepacked weights (0: sizes moe_mxfp4_gemm does not take)."""
+    _sizes("moe_mxfp4_weight_bytes", E, N, K)
+    return lib().moe_mxfp4_weight_bytes(E, N, K)
+
+
+def moe_mxfp4_weight_scale_bytes(E, N, K):
+    _sizes("moe_mxfp4_weight_scale_bytes", E, N, K)
+    return lib().moe_mxfp4_weight_scale_bytes(E, N, K)
+
+
+def moe_mxfp4_prepack(w, w_scales, E, N, K, w_tiled, w_scales_chunked, stream=None):
+    """Weights u8 [E, N, K/2] and scales u8 [E, N, K/32] -> the layout moe_mxfp4_gemm reads."""
+    _sizes("moe_mxfp4_prepack", E, N, K)
+    w, w_scales, w_tiled, w_scales_chunked = _buffers(
+        "moe_mxfp4_prepack", ("w", w, E * N * (K // 2), _U8),
+        ("w_scales", w_scales, E * N * (K // 32), _U8),
+        ("w_tiled", w_tiled, moe_mxfp4_weight_bytes(E, N, K), _U8),
+        ("w_scales_chunked", w_scales_chunked, moe_mxfp4_weight_scale_bytes(E, N, K), _U8))
+    _check(lib().moe_mxfp4_prepack(w, w_scales, E, N, K, w_tiled, w_scales_chunked,
+                                   _stream(stream)), "moe_mxfp4_prepack")
+
+
+def moe_mxfp4_workspace_bytes(R, E, N, K):
+    _sizes("moe_mxfp4_workspace_bytes", R, E, N, K)
+    return lib().moe_mxfp4_workspace_bytes(R, E, N, K)
+
+
+def moe_mxfp4_gemm(codes, scales, offsets, R, E, N, K, w_tiled, w_scales_chunked, dtype, out,
+                   workspace, stream=None):
+    """out[r] = a[r] @ w[e]^T for the rows r of expert e (offsets i32 [E+1]; None: one
+    group): codes u8 [R, K/2] with group-major scales, prepacked weights, out [R, N]
+    "bf16" or "fp16".  workspace: moe_mxfp4_workspace_bytes, zeroed before its first use."""
+    d = _choice("moe_mxfp4_gemm", "dtype", DTYPES, dtype)
+    _sizes("moe_mxfp4_gemm", R, E, N, K)
+    L = lib()
+    z, tt = _ELEM[dtype]
+    p = _buffers("moe_mxfp4_gemm", ("codes", codes, R * (K // 2), _U8),
+                 ("scales", scales, (K + 127) // 128 * R * 4, _U8),
+                 ("offsets", offsets, 4 * (E + 1), _I32),
+                 ("w_tiled", w_tiled, L.moe_mxfp4_weight_bytes(E, N, K), _U8),
+                 ("w_scales_chunked", w_scales_chunked, L.moe_mxfp4_weight_scale_bytes(E, N, K), _U8),
+                 ("out", out, R * N * z, tt),
+                 ("workspace", workspace, L.moe_mxfp4_workspace_bytes(R, E, N, K), None))
+    _check(L.moe_mxfp4_gemm(p[0], p[1], p[2], R, E, N, K, p[3], p[4], d, p[5], p[6],
+                            _stream(stream)), "moe_mxfp4_gemm")
+
+
+def moe_mxfp4_clear_error(workspace, stream=None):
+    _check(lib().moe_mxfp4_clear_error(_ptr(workspace), _stream(stream)), "moe_mxfp4_clear_error")
+
+
+def moe_mxfp4_check_error(workspace, stream=None):
+    """Synchronises the stream; returns the moe_status code (0 = no device error)."""
+    return lib().moe_mxfp4_check_error(_ptr(workspace), _stream(stream))
 
 
 def _expect(name, t, shape, dtype, device):

@@ -122,6 +122,14 @@ int sm_count();
 // device, once per (kernel, device); thread-safe.
 cudaError_t ensure_max_dynamic_smem(const void* kernel, int bytes);
 
+// Sizes the MXFP4 product and its weight layout take: whole 32-wide blocks of K,
+// output rows of whole 16-byte vectors, and tile counts that fit their types.
+constexpr int kMxMaxExperts = 256;
+inline bool mx_gemm_sizes_ok(int E, int N, int K) {
+  return E >= 1 && E <= kMxMaxExperts && N >= 1 && N <= (1 << 20) && N % 8 == 0 && K >= 1 &&
+         K <= (1 << 20) && K % 32 == 0;
+}
+
 // Kernel launchers (each returns the status of its own launches).
 cudaError_t launch_route(const moe_plan_s* p, const int32_t* topk_idx, uint8_t* ws,
                          cudaStream_t st);

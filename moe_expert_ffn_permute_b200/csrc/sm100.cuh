@@ -150,6 +150,13 @@ __device__ __forceinline__ void tma_load_2d(void* smem_dst, const CUtensorMap* m
       : "memory");
 }
 
+// cp.async of 4 bytes, or 4 zero bytes when `in` is false (nothing is read).
+__device__ __forceinline__ void cp_async_4_zfill(void* smem_dst, const void* gmem_src, bool in) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(smem_dst)),
+               "l"(gmem_src), "r"(in ? 4u : 0u)
+               : "memory");
+}
+
 __device__ __forceinline__ void bulk_load(void* smem_dst, const void* gmem_src, uint32_t bytes,
                                           uint64_t* bar) {
   asm volatile(
@@ -277,6 +284,32 @@ __device__ __forceinline__ void mma_mxf8f6f4(uint32_t d_tmem, uint64_t a_desc, u
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%5], [%6], p;\n\t"
+      "}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
+      : "memory");
+}
+
+// Instruction descriptor of tcgen05.mma.kind::mxf4.block_scale (scale_vec::2X),
+// M = 128, E2M1 A and B packed two to a byte and K-major, UE8M0 scales, K = 64
+// per instruction.  Each operand takes two scale bytes per row; its scale id (0
+// or 2) picks the half of the 32-bit scale word, here and in bits 30-31 of the
+// operand's TMEM scale address.
+//   bits 4-5 B scale id, 7-9 A format, 10-11 B format (1 = E2M1), 17-22 N >> 3,
+//   23 scale type (1 = UE8M0), 27-28 M >> 7, 29-30 A scale id, 31 K (0 = 64)
+__host__ __device__ constexpr uint32_t mxf4_idesc(uint32_t n, uint32_t sf_id) {
+  return (sf_id << 4) | (1u << 7) | (1u << 10) | ((n >> 3) << 17) | (1u << 23) | (1u << 27) |
+         (sf_id << 29);
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T, both MXFP4, K = 64 per instruction.
+__device__ __forceinline__ void mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                         uint32_t idesc, uint32_t sfa_tmem, uint32_t sfb_tmem,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], "
+      "[%6], p;\n\t"
       "}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
       : "memory");

@@ -1,0 +1,390 @@
+"""MXFP4 on the GPU: the quantiser byte for byte and the grouped product against
+oracle/rows.py in float64, and the chain of both with the row operators.
+
+The product's tolerance: every E2M1 x E2M1 product with power-of-two scales is
+exact in fp32; a K = 64 step of the tensor core adds 64 of them and the running
+sum, ceil(K / 64) times.  Taking each of those additions to keep 24 bits, rounded
+or cut (2^-23 relative to the magnitudes added), the sum is off by at most
+(64 + K / 64) * 2^-23 * sum |a w|; then one rounding to the output type (bf16
+2^-8, fp16 2^-11).  Whole-number cases, whose sums fit 24 bits, are bitwise."""
+import numpy as np
+import pytest
+import torch
+
+import moe_expert_ffn_permute_b200 as moe
+from oracle import rows as O
+
+from gpu_helpers import ensure_built
+from test_gpu_rows import DT, HALF, TINY, _gen, _np, _route
+
+pytestmark = pytest.mark.gpu
+
+
+def _quantize(x, dtype, layout, k=1, inv=None, fill=0xEE):
+    T, K = x.shape
+    R = T * k
+    codes = torch.full((R, K // 2), fill, dtype=torch.uint8, device="cuda")
+    scales = torch.full(moe.mxfp4_scale_shape(R, K, layout), fill, dtype=torch.uint8, device="cuda")
+    moe.moe_quantize_mxfp4(x, dtype, T, K, k, inv, codes, scales, layout)
+    return codes, scales
+
+
+def _hard(T, K, dtype, seed):
+    """Values of many magnitudes with exact ties, zeros, block maxima on a
+    boundary, subnormals and blocks that are not finite."""
+    g = _gen(seed)
+    x = torch.randn(T, K, generator=g, device="cuda")
+    x = x * torch.exp2(torch.randint(-12, 13, (T, K // 32, 1), generator=g, device="cuda").float()
+                       ).expand(T, K // 32, 32).reshape(T, K)
+    b = x.view(T, K // 32, 32)
+    ties = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0], device="cuda").repeat(4)
+    b[0, 0] = ties
+    if T > 1:
+        b[1, 0] = -ties * 2.0 ** -10
+        b[1, -1] = 0.0
+    if T > 2:
+        b[2, 0] = 0.0
+        b[2, 0, 5] = 6.0 * 2.0 ** -14 if dtype == "fp16" else 6.0 * 2.0 ** -120
+        b[2, -1, 0] = float("nan")
+    if T > 3:
+        b[3, 0, 31] = float("inf")
+        b[3, -1, :] = 2.0 ** -24 if dtype == "fp16" else 2.0 ** -133
+    if T > 4:
+        b[4, 0, 7] = 65504.0 if dtype == "fp16" else 3.0e38
+    return x.to(DT[dtype])
+
+
+@pytest.mark.parametrize("layout", ["row", "group"])
+@pytest.mark.parametrize("dtype,T,K", [("bf16", 1, 32), ("fp16", 5, 32), ("fp32", 7, 64),
+                                       ("bf16", 300, 96), ("bf16", 6, 7168), ("fp32", 33, 1568),
+                                       ("fp16", 129, 160), ("bf16", 9, 128)])
+def test_quantize_and_dequantize(dtype, T, K, layout):
+    ensure_built()
+    x = _hard(T, K, dtype, T * 17 + K)
+    codes, scales = _quantize(x, dtype, layout)
+    want_c, want_s = O.quantize_mxfp4(_np(x))
+    np.testing.assert_array_equal(codes.cpu().numpy(), want_c)
+    np.testing.assert_array_equal(scales.cpu().numpy(),
+                                  want_s if layout == "row" else O.group_major(want_s))
+    val = O.dequantize_mxfp4(want_c, want_s)
+    for out_t in ("bf16", "fp32", "fp16"):
+        out = torch.empty(T, K, dtype=DT[out_t], device="cuda")
+        moe.moe_dequantize_mxfp4(codes, scales, layout, T, K, out_t, out)
+        # Exact but for the range: codes of values near fp32's largest can stand for
+        # 4 * 2^126 = 2^128, which rounds to infinity in bf16 and fp32 too.
+        with np.errstate(over="ignore"):
+            want = val.astype(np.float16 if out_t == "fp16" else np.float32).astype(np.float64)
+        np.testing.assert_array_equal(_np(out), want)
+
+
+def test_every_code_and_scale():
+    ensure_built()
+    codes = torch.arange(256, dtype=torch.uint8, device="cuda")[:, None].expand(256, 16).contiguous()
+    scales = torch.arange(256, dtype=torch.uint8, device="cuda")[:, None].contiguous()
+    for flip in (0, 85):
+        c = torch.roll(codes, flip, 0).contiguous()
+        out = torch.empty(256, 32, dtype=torch.float32, device="cuda")
+        moe.moe_dequantize_mxfp4(c, scales, "row", 256, 32, "fp32", out)
+        with np.errstate(over="ignore"):
+            want = O.dequantize_mxfp4(c.cpu().numpy(), scales.cpu().numpy()).astype(np.float32)
+        np.testing.assert_array_equal(out.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("layout", ["row", "group"])
+@pytest.mark.parametrize("dtype,T,K,k,E,masked", [("bf16", 1, 7168, 8, 32, 0.0),
+                                                   ("fp16", 37, 96, 3, 8, 0.3),
+                                                   ("fp32", 130, 288, 12, 16, 0.5),
+                                                   ("bf16", 9, 64, 2, 4, 1.1)])
+def test_quantize_into_expert_order(dtype, T, K, k, E, masked, layout):
+    """Equals quantising in token order and copying; other rows are untouched."""
+    ensure_built()
+    g = _gen(T + K)
+    inv, _ = _route(T, k, E, masked, g)
+    x = _hard(T, K, dtype, 3)
+    codes, scales = _quantize(x, dtype, layout, k, inv)
+    want_c, want_s = O.quantize_mxfp4(_np(x))
+    iv = inv.cpu().numpy()
+    rc = O.permute(want_c, iv, np.full((T * k, K // 2), 0xEE, np.uint8))
+    np.testing.assert_array_equal(codes.cpu().numpy(), rc)
+    if layout == "row":
+        rs = O.permute(want_s, iv, np.full((T * k, K // 32), 0xEE, np.uint8))
+    else:
+        gm = O.group_major(want_s)
+        rs = np.stack([O.permute(gm[i], iv, np.full((T * k, 4), 0xEE, np.uint8))
+                       for i in range(len(gm))])
+    np.testing.assert_array_equal(scales.cpu().numpy(), rs)
+
+
+def test_quantize_offsets_past_32_bits():
+    """More than 2^32 codes and 2^31 bytes of them; checked on rows from both ends."""
+    ensure_built()
+    T, K, k = 640, 7168, 1024
+    g = _gen(4)
+    x = torch.randn(T, K, generator=g, device="cuda").to(torch.bfloat16)
+    inv = torch.randperm(T * k, generator=g, device="cuda").to(torch.int32).reshape(T, k).contiguous()
+    codes, scales = _quantize(x, "bf16", "group", k, inv)
+    base_c, base_s = _quantize(x, "bf16", "group")
+    for t in (0, 1, 320, T - 1):
+        at = inv[t].long()
+        assert torch.equal(codes[at], base_c[t].expand(k, -1))
+        assert torch.equal(scales[:, at], base_s[:, t:t + 1].expand(-1, k, -1))
+    R = T * k
+    out = torch.empty(R, K, dtype=torch.bfloat16, device="cuda")
+    moe.moe_dequantize_mxfp4(codes, scales, "group", R, K, "bf16", out)
+    one = torch.empty(T, K, dtype=torch.bfloat16, device="cuda")
+    moe.moe_dequantize_mxfp4(base_c, base_s, "group", T, K, "bf16", one)
+    for t in (0, T - 1):
+        assert torch.equal(out[inv[t].long()], one[t].expand(k, -1))
+
+
+# --------------------------------------------------------------------- product
+def _operands(R, E, N, K, seed, whole=False):
+    """Codes and row-major scales of rows and weights (numpy).  whole: scales
+    2^-1 .. 2^1, so that all sums are exact in fp32 for K <= 1024."""
+    g = np.random.default_rng(seed)
+
+    def draw(n):
+        codes = g.integers(0, 256, (n, K // 2), dtype=np.uint8)
+        lo, hi = (126, 129) if whole else (118, 126)
+        return codes, g.integers(lo, hi, (n, K // 32)).astype(np.uint8)
+
+    a, sa = draw(R)
+    w, sw = draw(E * N)
+    return a, sa, w.reshape(E, N, K // 2), sw.reshape(E, N, K // 32)
+
+
+def _cuda(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+class Product:
+    def __init__(self, R, E, N, K, a, sa, w, sw):
+        self.R, self.E, self.N, self.K = R, E, N, K
+        self.codes, self.scales = _cuda(a), _cuda(O.group_major(sa))
+        self.w = torch.empty(moe.moe_mxfp4_weight_bytes(E, N, K), dtype=torch.uint8, device="cuda")
+        self.ws = torch.empty(moe.moe_mxfp4_weight_scale_bytes(E, N, K), dtype=torch.uint8,
+                              device="cuda")
+        moe.moe_mxfp4_prepack(_cuda(w), _cuda(sw), E, N, K, self.w, self.ws)
+        self.workspace = torch.zeros(moe.moe_mxfp4_workspace_bytes(R, E, N, K), dtype=torch.uint8,
+                                     device="cuda")
+
+    def __call__(self, offsets, dtype, out=None):
+        if out is None:
+            out = torch.full((self.R, self.N), 7.0, dtype=DT[dtype], device="cuda")
+        moe.moe_mxfp4_gemm(self.codes, self.scales, offsets, self.R, self.E, self.N, self.K, self.w,
+                           self.ws, dtype, out, self.workspace)
+        return out
+
+    def check(self):
+        assert moe.moe_mxfp4_check_error(self.workspace) == 0
+
+
+def _offsets(counts, lead=0):
+    return np.concatenate([[lead], lead + np.cumsum(counts)]).astype(np.int32)
+
+
+# (counts, rows behind the last group, N, K): tile edges of 16, 64, 128 and 256
+# rows on both tile variants (few rows per expert, many), groups without rows at
+# the ends and in between, K inside and across the 128- and 256-wide blocks, N
+# inside and across the 128-row weight blocks.
+PRODUCTS = [
+    ([1], 0, 8, 32), ([1], 3, 128, 256), ([2, 0, 1], 0, 136, 64), ([0, 15, 16, 17, 0], 2, 128, 96),
+    ([63, 64, 65], 1, 264, 288), ([0, 0, 0], 4, 128, 128), ([33] * 40, 0, 64, 160),
+    ([127, 1, 128], 0, 128, 512), ([129, 255, 256, 257], 5, 120, 320), ([700], 0, 384, 224),
+    ([0, 513, 0, 3], 0, 256, 1024), ([2] * 256, 0, 40, 96), ([300, 0, 1], 0, 1160, 672),
+]
+PIDS = [f"p{i}-N{p[2]}-K{p[3]}" for i, p in enumerate(PRODUCTS)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("counts,behind,N,K", PRODUCTS, ids=PIDS)
+def test_product_whole_numbers_bitwise(counts, behind, N, K, dtype):
+    ensure_built()
+    E, R = len(counts), sum(counts) + behind
+    a, sa, w, sw = _operands(R, E, N, K, R + N + K, whole=True)
+    off = _offsets(counts)
+    p = Product(R, E, N, K, a, sa, w, sw)
+    out = p(_cuda(off), dtype)
+    p.check()
+    want = O.grouped_product(O.dequantize_mxfp4(a, sa), O.dequantize_mxfp4(w.reshape(E * N, -1),
+                             sw.reshape(E * N, -1)).reshape(E, N, K), off, np.full((R, N), 7.0))
+    want = torch.from_numpy(want).to(DT[dtype])       # exact sums: one rounding
+    assert torch.equal(out.cpu(), want), (out.cpu() != want).nonzero()[:8]
+    if E == 1 and behind == 0:
+        assert torch.equal(p(None, dtype), out)       # one group: offsets not needed
+
+
+@pytest.mark.parametrize("counts,behind,N,K", [([5, 40, 0, 9], 0, 264, 2080), ([200, 90], 0, 128, 7168),
+                                               ([1], 0, 512, 7168), ([777], 0, 136, 2048),
+                                               ([3] * 32, 1, 256, 1536)])
+def test_product_of_quantised_values(counts, behind, N, K):
+    """Normal values quantised on the GPU, within the derived tolerance."""
+    ensure_built()
+    E, R = len(counts), sum(counts) + behind
+    g = _gen(R + K)
+    x = torch.randn(R, K, generator=g, device="cuda").to(torch.bfloat16)
+    wt = (torch.randn(E * N, K, generator=g, device="cuda") * 0.02)
+    a, sa = _quantize(x, "bf16", "row")
+    w, sw = _quantize(wt, "fp32", "row")
+    a, sa, w, sw = (t.cpu().numpy() for t in (a, sa, w, sw))
+    off = _offsets(counts)
+    p = Product(R, E, N, K, a, sa, w.reshape(E, N, -1), sw.reshape(E, N, -1))
+    av, wv = O.dequantize_mxfp4(a, sa), O.dequantize_mxfp4(w, sw).reshape(E, N, K)
+    want = O.grouped_product(av, wv, off, np.full((R, N), 7.0))
+    mag = O.grouped_product(np.abs(av), np.abs(wv), off, np.zeros((R, N)))
+    for dtype in ("bf16", "fp16"):
+        out = p(_cuda(off), dtype)
+        p.check()
+        tol = 1.01 * ((64 + K / 64) * 2.0 ** -23 * mag + HALF[dtype] * np.abs(want)) + TINY[dtype]
+        err = np.abs(_np(out) - want)
+        assert (err <= tol).all(), (err.max(), (err / tol).max())
+        assert torch.equal(p(_cuda(off), dtype), out)      # repeats bitwise
+
+
+def test_product_offsets_that_are_not_prefix_sums():
+    """Offsets that start late, run backwards or out of range stay in bounds and
+    mean what their clamped, non-decreasing values say."""
+    ensure_built()
+    R, E, N, K = 100, 4, 128, 256
+    a, sa, w, sw = _operands(R, E, N, K, 1, whole=True)
+    p = Product(R, E, N, K, a, sa, w, sw)
+    av = O.dequantize_mxfp4(a, sa)
+    wv = O.dequantize_mxfp4(w.reshape(E * N, -1), sw.reshape(E * N, -1)).reshape(E, N, K)
+    for off in ([10, 20, 20, 90, 95], [-5, 30, 7, 60, 1 << 30], [100] * 5, [50, 0, 0, 0, 0],
+                [0, 1 << 31 - 1, 3, 5, 100]):
+        off = np.array(off, np.int64).astype(np.int32)
+        out = p(_cuda(off), "bf16")
+        p.check()
+        want = torch.from_numpy(O.grouped_product(av, wv, off, np.full((R, N), 7.0))).bfloat16()
+        assert torch.equal(out.cpu(), want), off
+
+
+def test_product_keeps_nan_rows_apart():
+    """A NaN scale (a row whose block was not finite) makes that row NaN and no
+    other; a NaN weight scale that output feature."""
+    ensure_built()
+    R, E, N, K = 40, 1, 136, 320
+    a, sa, w, sw = _operands(R, E, N, K, 2, whole=True)
+    clean = Product(R, E, N, K, a, sa, w, sw)(None, "bf16")
+    sa[17, 3], sw[0, 130, 9] = 255, 255
+    out = Product(R, E, N, K, a, sa, w, sw)(None, "bf16")
+    nan = torch.isnan(out)
+    want = torch.zeros_like(nan)
+    want[17], want[:, 130] = True, True
+    assert torch.equal(nan, want)
+    assert torch.equal(out[~want], clean[~want])
+
+
+def test_product_in_two_graphs_and_on_two_streams():
+    """Two captured products with workspaces of their own, replayed on two streams
+    at once, equal the eager calls; one workspace serves calls in order."""
+    ensure_built()
+    cases = [([40] * 32, 256, 1024), ([600, 300], 512, 768)]
+    ps, offs, want, outs, graphs = [], [], [], [], []
+    for i, (counts, N, K) in enumerate(cases):
+        R, E = sum(counts), len(counts)
+        ps.append(Product(R, E, N, K, *_operands(R, E, N, K, 50 + i)))
+        offs.append(_cuda(_offsets(counts)))
+        want.append(ps[i](offs[i], "bf16"))
+        outs.append(torch.zeros_like(want[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for _ in range(3):
+                ps[i](offs[i], "bf16", outs[i])
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for i in range(2):
+            assert torch.equal(outs[i], want[i])
+            ps[i].check()
+
+
+def test_expert_ffn_chain():
+    """The operators as a user runs them: route, quantise into expert order, gate-up
+    product, SwiGLU, quantise, down product, weighted sum back -- against the same
+    chain in float64 (on the GPU's own 4-bit codes of the activation, which rounding
+    decides)."""
+    ensure_built()
+    T, H, I, E, k = 70, 512, 256, 8, 3
+    g = _gen(77)
+    inv, offsets = _route(T, k, E, 0.1, g)
+    S = T * k
+    x = torch.randn(T, H, generator=g, device="cuda").to(torch.bfloat16)
+    tw = torch.softmax(torch.randn(T, k, generator=g, device="cuda"), 1)
+    ws = []
+    for rows, cols in ((2 * I, H), (H, I)):
+        wt = torch.randn(E * rows, cols, generator=g, device="cuda") * 0.05
+        c, s = _quantize(wt, "fp32", "row")
+        ws.append((c.reshape(E, rows, -1), s.reshape(E, rows, -1)))
+
+    def layer(w, sw, N, K):
+        wt = torch.empty(moe.moe_mxfp4_weight_bytes(E, N, K), dtype=torch.uint8, device="cuda")
+        st = torch.empty(moe.moe_mxfp4_weight_scale_bytes(E, N, K), dtype=torch.uint8, device="cuda")
+        moe.moe_mxfp4_prepack(w, sw, E, N, K, wt, st)
+        return wt, st
+
+    w1, w2 = layer(*ws[0], 2 * I, H), layer(*ws[1], H, I)
+    space = torch.zeros(max(moe.moe_mxfp4_workspace_bytes(S, E, 2 * I, H),
+                            moe.moe_mxfp4_workspace_bytes(S, E, H, I)), dtype=torch.uint8,
+                        device="cuda")
+    codes = torch.zeros(S, H // 2, dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(moe.mxfp4_scale_shape(S, H, "group"), dtype=torch.uint8, device="cuda")
+    moe.moe_quantize_mxfp4(x, "bf16", T, H, k, inv, codes, scales, "group")
+    h = torch.zeros(S, 2 * I, dtype=torch.bfloat16, device="cuda")
+    moe.moe_mxfp4_gemm(codes, scales, offsets, S, E, 2 * I, H, *w1, "bf16", h, space)
+    act = (torch.nn.functional.silu(h[:, :I].float()) * h[:, I:].float()).to(torch.bfloat16)
+    c2, s2 = _quantize(act, "bf16", "group")
+    y = torch.zeros(S, H, dtype=torch.bfloat16, device="cuda")
+    moe.moe_mxfp4_gemm(c2, s2, offsets, S, E, H, I, *w2, "bf16", y, space)
+    out = torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
+    moe.moe_unpermute(y, "bf16", T, H, k, inv, tw, out)
+    assert moe.moe_mxfp4_check_error(space) == 0
+
+    iv, off = inv.cpu().numpy(), offsets.cpu().numpy()
+    qc, qs = O.quantize_mxfp4(_np(x))
+    a = O.permute(O.dequantize_mxfp4(qc, qs), iv, np.zeros((S, H)))
+    val = [O.dequantize_mxfp4(c.cpu().numpy(), s.cpu().numpy()) for c, s in ws]
+    h64 = O.grouped_product(a, val[0], off, np.zeros((S, 2 * I)))
+    mag = O.grouped_product(np.abs(a), np.abs(val[0]), off, np.zeros((S, 2 * I)))
+    tol = 1.01 * ((64 + H / 64) * 2.0 ** -23 * mag + HALF["bf16"] * np.abs(h64)) + TINY["bf16"]
+    assert (np.abs(_np(h) - h64) <= tol).all()
+    a2c, a2s = O.quantize_mxfp4(_np(act))
+    np.testing.assert_array_equal(c2.cpu().numpy(), a2c)
+    a2 = O.dequantize_mxfp4(a2c, a2s)
+    y64 = O.grouped_product(a2, val[1], off, np.zeros((S, H)))
+    mag = O.grouped_product(np.abs(a2), np.abs(val[1]), off, np.zeros((S, H)))
+    tol = 1.01 * ((64 + I / 64) * 2.0 ** -23 * mag + HALF["bf16"] * np.abs(y64)) + TINY["bf16"]
+    assert (np.abs(_np(y) - y64) <= tol).all()
+    # The sum takes the GPU's rows: k multiply-adds and one rounding.
+    w64 = _np(tw)
+    want = O.unpermute(_np(y), iv, w64)
+    mag = O.unpermute(np.abs(_np(y)), iv, np.abs(w64))
+    assert (np.abs(_np(out) - want) <= 1.01 * (k * 2.0 ** -24 * mag + HALF["bf16"] * np.abs(want))
+            + TINY["bf16"]).all()
+
+
+def test_tensor_checks_on_the_gpu():
+    ensure_built()
+    R, E, N, K = 8, 2, 64, 64
+    p = Product(R, E, N, K, *_operands(R, E, N, K, 3))
+    off = _cuda(_offsets([4, 4]))
+    out = torch.zeros(R, N, dtype=torch.bfloat16, device="cuda")
+    args = dict(codes=p.codes, scales=p.scales, offsets=off, R=R, E=E, N=N, K=K, w_tiled=p.w,
+                w_scales_chunked=p.ws, dtype="bf16", out=out, workspace=p.workspace)
+    moe.moe_mxfp4_gemm(**args)
+    for over in (dict(codes=p.codes[:4]), dict(scales=p.scales[:, :4]), dict(offsets=off.long()),
+                 dict(offsets=off[:2]), dict(w_tiled=p.w[:-1]), dict(w_scales_chunked=p.ws[:512]),
+                 dict(dtype="fp16"), dict(out=out[:4]), dict(out=out.t()), dict(workspace=p.workspace[:128]),
+                 dict(R=9), dict(N=72, out=torch.zeros(R, 72, dtype=torch.bfloat16).cuda(), w_tiled=p.w[:1])):
+        with pytest.raises(moe.MoEError) as e:
+            moe.moe_mxfp4_gemm(**{**args, **over})
+        assert e.value.status == moe.MOE_ERR_INVALID_ARG, over

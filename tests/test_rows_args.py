@@ -1,0 +1,123 @@
+"""Refusals of the row operators and the MXFP4 operators, without a GPU: sizes,
+pointers, alignment and overlap by the C ABI (raw addresses; nothing is launched),
+tensors by the binding."""
+import pytest
+import torch
+
+import moe_expert_ffn_permute_b200 as moe
+from moe_expert_ffn_permute_b200.build import build
+
+INVALID, UNSUPPORTED, ALIGNMENT = 1, 2, 3
+A, B, C, D, E_, F_, G = (1 << 40, 2 << 40, 3 << 40, 4 << 40, 5 << 40, 6 << 40, 7 << 40)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build()
+
+
+def _refused(status, fn, **over):
+    base = {
+        "moe_permute": dict(x=A, T=4, row_bytes=256, k=2, inv=B, rows=C),
+        "moe_permute_backward": dict(drows=A, dtype="bf16", T=4, H=64, k=2, inv=B, dx=C),
+        "moe_unpermute": dict(rows=A, dtype="bf16", T=4, H=64, k=2, inv=B, topk_w=C, out=D),
+        "moe_unpermute_backward": dict(dout=A, rows=B, dtype="bf16", T=4, H=64, k=2, inv=C,
+                                       topk_w=D, drows=E_, dw=F_),
+        "moe_quantize_mxfp4": dict(x=A, dtype="bf16", T=4, K=64, k=2, inv=B, codes=C, scales=D,
+                                   scale_layout="group"),
+        "moe_dequantize_mxfp4": dict(codes=A, scales=B, scale_layout="row", R=4, K=64,
+                                     dtype="bf16", out=C),
+        "moe_mxfp4_prepack": dict(w=A, w_scales=B, E=2, N=64, K=64, w_tiled=C,
+                                  w_scales_chunked=D),
+        "moe_mxfp4_gemm": dict(codes=A, scales=B, offsets=C, R=8, E=2, N=64, K=64, w_tiled=D,
+                               w_scales_chunked=E_, dtype="bf16", out=F_, workspace=G),
+    }[fn]
+    base.update(over)
+    with pytest.raises(moe.MoEError) as e:
+        getattr(moe, fn)(**base, stream=0)
+    assert e.value.status == status, (fn, over, e.value)
+
+
+CASES = [
+    ("moe_permute", INVALID, dict(x=None)), ("moe_permute", INVALID, dict(inv=None)),
+    ("moe_permute", INVALID, dict(rows=None)), ("moe_permute", INVALID, dict(T=0)),
+    ("moe_permute", INVALID, dict(k=0)), ("moe_permute", INVALID, dict(row_bytes=0)),
+    ("moe_permute", INVALID, dict(T=1 << 30, k=2)), ("moe_permute", INVALID, dict(T=1 << 31)),
+    ("moe_permute", UNSUPPORTED, dict(row_bytes=18)), ("moe_permute", ALIGNMENT, dict(x=A + 8)),
+    ("moe_permute", ALIGNMENT, dict(rows=C + 4)), ("moe_permute", ALIGNMENT, dict(inv=B + 2)),
+    ("moe_permute", INVALID, dict(rows=A)), ("moe_permute", INVALID, dict(rows=A + 1008)),
+    ("moe_permute", UNSUPPORTED, dict(T=1 << 30, k=1, row_bytes=1 << 44)),
+    ("moe_permute_backward", INVALID, dict(drows=None)),
+    ("moe_permute_backward", INVALID, dict(dx=None)),
+    ("moe_permute_backward", INVALID, dict(dtype="fp8")),
+    ("moe_permute_backward", INVALID, dict(dx=A + 16)),
+    ("moe_permute_backward", UNSUPPORTED, dict(H=63)),
+    ("moe_permute_backward", UNSUPPORTED, dict(dtype="fp32", H=62)),
+    ("moe_permute_backward", ALIGNMENT, dict(dx=C + 8)),
+    ("moe_unpermute", INVALID, dict(topk_w=None)), ("moe_unpermute", INVALID, dict(inv=None)),
+    ("moe_unpermute", INVALID, dict(T=-1)), ("moe_unpermute", INVALID, dict(H=0)),
+    ("moe_unpermute", INVALID, dict(k=-3)), ("moe_unpermute", INVALID, dict(dtype=torch.bfloat16)),
+    ("moe_unpermute", ALIGNMENT, dict(topk_w=C + 1)), ("moe_unpermute", UNSUPPORTED, dict(H=4)),
+    ("moe_unpermute_backward", INVALID, dict(drows=None, dw=None)),
+    ("moe_unpermute_backward", INVALID, dict(rows=None)),
+    ("moe_unpermute_backward", INVALID, dict(topk_w=None)),
+    ("moe_unpermute_backward", INVALID, dict(drows=A)),
+    ("moe_unpermute_backward", INVALID, dict(drows=B)),
+    ("moe_unpermute_backward", INVALID, dict(dw=E_ + 16)),
+    ("moe_unpermute_backward", ALIGNMENT, dict(dw=F_ + 2)),
+    ("moe_unpermute_backward", UNSUPPORTED, dict(H=20)),
+    ("moe_quantize_mxfp4", INVALID, dict(inv=None)), ("moe_quantize_mxfp4", INVALID, dict(x=None)),
+    ("moe_quantize_mxfp4", INVALID, dict(scale_layout="col")),
+    ("moe_quantize_mxfp4", INVALID, dict(T=0)), ("moe_quantize_mxfp4", INVALID, dict(codes=A)),
+    ("moe_quantize_mxfp4", INVALID, dict(scales=C)),
+    ("moe_quantize_mxfp4", UNSUPPORTED, dict(K=48)),
+    ("moe_quantize_mxfp4", ALIGNMENT, dict(scales=D + 2)),
+    ("moe_quantize_mxfp4", ALIGNMENT, dict(codes=C + 8)),
+    ("moe_dequantize_mxfp4", INVALID, dict(R=0)), ("moe_dequantize_mxfp4", INVALID, dict(out=A)),
+    ("moe_dequantize_mxfp4", INVALID, dict(out=B)), ("moe_dequantize_mxfp4", INVALID, dict(scales=None)),
+    ("moe_dequantize_mxfp4", UNSUPPORTED, dict(K=16)),
+    ("moe_dequantize_mxfp4", ALIGNMENT, dict(out=C + 4)),
+    ("moe_mxfp4_prepack", INVALID, dict(w=None)), ("moe_mxfp4_prepack", INVALID, dict(E=0)),
+    ("moe_mxfp4_prepack", UNSUPPORTED, dict(E=257)), ("moe_mxfp4_prepack", UNSUPPORTED, dict(N=12)),
+    ("moe_mxfp4_prepack", UNSUPPORTED, dict(K=40)), ("moe_mxfp4_prepack", ALIGNMENT, dict(w=A + 8)),
+    ("moe_mxfp4_prepack", INVALID, dict(w_tiled=A)), ("moe_mxfp4_prepack", INVALID, dict(w_tiled=B)),
+    ("moe_mxfp4_prepack", INVALID, dict(w_scales_chunked=C)),
+    ("moe_mxfp4_gemm", INVALID, dict(offsets=None)), ("moe_mxfp4_gemm", INVALID, dict(workspace=None)),
+    ("moe_mxfp4_gemm", INVALID, dict(R=0)), ("moe_mxfp4_gemm", INVALID, dict(dtype="fp8")),
+    ("moe_mxfp4_gemm", UNSUPPORTED, dict(dtype="fp32")), ("moe_mxfp4_gemm", UNSUPPORTED, dict(N=4)),
+    ("moe_mxfp4_gemm", UNSUPPORTED, dict(K=16)), ("moe_mxfp4_gemm", UNSUPPORTED, dict(E=300)),
+    ("moe_mxfp4_gemm", INVALID, dict(out=A)), ("moe_mxfp4_gemm", INVALID, dict(out=B)),
+    ("moe_mxfp4_gemm", ALIGNMENT, dict(workspace=G + 128)),
+    ("moe_mxfp4_gemm", ALIGNMENT, dict(codes=A + 8)), ("moe_mxfp4_gemm", ALIGNMENT, dict(out=F_ + 2)),
+]
+
+
+@pytest.mark.parametrize("fn,status,over", CASES,
+                         ids=[f"{f[4:]}-{'-'.join(map(str, o))}-{i}" for i, (f, _, o) in enumerate(CASES)])
+def test_refused(fn, status, over):
+    _refused(status, fn, **over)
+
+
+def test_tensors_on_the_cpu_are_refused():
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    _refused(INVALID, "moe_permute", x=x)
+    _refused(INVALID, "moe_unpermute", out=x)
+    _refused(INVALID, "moe_quantize_mxfp4", x=x)
+    _refused(INVALID, "moe_mxfp4_gemm", codes=torch.zeros(8, 32, dtype=torch.uint8))
+
+
+def test_sizes_that_do_not_fit_are_refused():
+    _refused(INVALID, "moe_unpermute", T=(1 << 32) + 4)
+    _refused(INVALID, "moe_mxfp4_gemm", K=(1 << 32) + 64)
+
+
+def test_sizes_of_prepacked_weights():
+    assert moe.moe_mxfp4_weight_bytes(3, 136, 288) == 3 * 2 * 2 * 16384
+    assert moe.moe_mxfp4_weight_scale_bytes(3, 128, 288) == 3 * 1 * 2 * 1024
+    for E, N, K in ((0, 128, 256), (257, 128, 256), (1, 12, 256), (1, 128, 48), (1, 0, 256),
+                    (1, 128, 0), (1, -8, 256), (1, (1 << 20) + 8, 256), (1, 8, (1 << 20) + 32)):
+        assert moe.moe_mxfp4_weight_bytes(E, N, K) == 0
+        assert moe.moe_mxfp4_weight_scale_bytes(E, N, K) == 0
+        assert moe.moe_mxfp4_workspace_bytes(4, E, N, K) == 0
+    assert moe.moe_mxfp4_workspace_bytes(0, 1, 128, 256) == 0
+    assert moe.moe_mxfp4_workspace_bytes(1, 1, 128, 256) >= 256
