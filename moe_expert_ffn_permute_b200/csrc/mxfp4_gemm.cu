@@ -141,7 +141,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_launch_dependents();
   Smem<kTok>& sm = *reinterpret_cast<Smem<kTok>*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  const int warp = threadIdx.x >> 5;
+  // (The shuffle makes the warp's number uniform to the compiler.)
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
   const int lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -210,28 +211,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   const long long tiles = static_cast<long long>(sm.tile_off[p.E]) * p.nb_n;
   const int kb_n = p.kb_n;
 
+  // The issuing warps run warp-uniform loops and elect a lane for the copies and
+  // MMAs alone (elect_one() says what that saves).
   if (warp == 0) {
     // ------------------------------------------------------------- operands
-    if (lane == 0) {
-      const uint64_t pol_tok = l2_policy_evict_last();
-      const uint64_t pol_once = l2_policy_evict_first();
-      const uint64_t pol_reused = l2_policy_evict_normal();
-      int stage = 0;
-      uint32_t phase = 0;
-      long long issued = 0;   // stages filled
-      bool ok = true;
-      for (long long id = blockIdx.x; ok && id < tiles; id += gridDim.x) {
-        const Tile t = tile_at<kTok>(sm, p, id);
-        // Weights of an expert with one token tile are read once.
-        const uint64_t pol_w = sm.tile_off[t.e + 1] - sm.tile_off[t.e] > 1 ? pol_reused : pol_once;
-        const int boxes = (t.rows + C::kBox - 1) / C::kBox;
-        const uint32_t bytes = kTileBytes + 1024 + boxes * C::kBox * kKBytes;
-        const size_t block = (static_cast<size_t>(t.e) * p.nb_n + t.nb) * kb_n;
-        for (int kb = 0; kb < kb_n; ++kb) {
-          if (!mbar_wait(&sm.empty[stage], phase ^ 1u, p.err, &sm.abort_flag)) {
-            ok = false;
-            break;
-          }
+    const uint64_t pol_tok = l2_policy_evict_last();
+    const uint64_t pol_once = l2_policy_evict_first();
+    const uint64_t pol_reused = l2_policy_evict_normal();
+    int stage = 0;
+    uint32_t phase = 0;
+    long long issued = 0;   // stages filled
+    bool ok = true;
+    for (long long id = blockIdx.x; ok && id < tiles; id += gridDim.x) {
+      const Tile t = tile_at<kTok>(sm, p, id);
+      // Weights of an expert with one token tile are read once.
+      const uint64_t pol_w = sm.tile_off[t.e + 1] - sm.tile_off[t.e] > 1 ? pol_reused : pol_once;
+      const int boxes = (t.rows + C::kBox - 1) / C::kBox;
+      const uint32_t bytes = kTileBytes + 1024 + boxes * C::kBox * kKBytes;
+      const size_t block = (static_cast<size_t>(t.e) * p.nb_n + t.nb) * kb_n;
+      for (int kb = 0; kb < kb_n; ++kb) {
+        if (!mbar_wait_warp(&sm.empty[stage], phase ^ 1u, p.err, &sm.abort_flag)) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
           mbar_arrive_expect_tx(&sm.full[stage], bytes);
           bulk_load_hint(sm.w[stage], p.w + (block + kb) * kTileBytes, kTileBytes, &sm.full[stage],
                          pol_w);
@@ -239,22 +242,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int b = 0; b < boxes; ++b)
             tma_load_2d(sm.t[stage] + b * C::kBox * kKBytes, &tmap, kb * kKBytes,
                         t.row + b * C::kBox, &sm.full[stage], pol_tok);
-          ++issued;
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
         }
-      }
-      // On the way out of an aborted CTA: its copies in flight land before its
-      // shared memory is given back.
-      for (int s = 0; !ok && s < STAGES && s < issued; ++s) {
-        if (--stage < 0) {
-          stage = STAGES - 1;
+        __syncwarp();
+        ++issued;
+        if (++stage == STAGES) {
+          stage = 0;
           phase ^= 1u;
         }
-        mbar_wait_limited(&sm.full[stage], phase, kWaitLimitNs);
       }
+    }
+    // On the way out of an aborted CTA: its copies in flight land before its
+    // shared memory is given back.
+    for (int s = 0; !ok && s < STAGES && s < issued; ++s) {
+      if (--stage < 0) {
+        stage = STAGES - 1;
+        phase ^= 1u;
+      }
+      mbar_wait_limited(&sm.full[stage], phase, kWaitLimitNs);
     }
     __syncwarp();
   } else if (warp == 2 || warp == 3) {
@@ -294,32 +298,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issue
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0, acc_phase = 0, set = 0;
-      const uint64_t w_desc0 = umma_desc_sw128(smem_u32(sm.w[0]));
-      const uint64_t t_desc0 = umma_desc_sw128(smem_u32(sm.t[0]));
-      const uint64_t sfw_desc0 = sf_desc(smem_u32(sm.sfw[0]));
-      const uint64_t sft_desc0 = sf_desc(smem_u32(sm.sft[0]));
-      constexpr uint64_t kKStep = 32 >> 4, kSfChunk = 512 >> 4;
-      bool ok = true;
-      for (long long id = blockIdx.x; ok && id < tiles; id += gridDim.x) {
-        const Tile t = tile_at<kTok>(sm, p, id);
-        const uint32_t n = mma_n(t.rows);
-        const uint32_t idesc0 = mxf4_idesc(n, 0);
-        if (!mbar_wait(&sm.tmem_empty, acc_phase ^ 1u, p.err, &sm.abort_flag)) break;
+    int stage = 0;
+    uint32_t phase = 0, acc_phase = 0, set = 0;
+    const uint32_t acc = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint64_t w_desc0 = umma_desc_sw128(smem_u32(sm.w[0]));
+    const uint64_t t_desc0 = umma_desc_sw128(smem_u32(sm.t[0]));
+    const uint64_t sfw_desc0 = sf_desc(smem_u32(sm.sfw[0]));
+    const uint64_t sft_desc0 = sf_desc(smem_u32(sm.sft[0]));
+    constexpr uint64_t kKStep = 32 >> 4, kSfChunk = 512 >> 4;
+    bool ok = true;
+    for (long long id = blockIdx.x; ok && id < tiles; id += gridDim.x) {
+      const Tile t = tile_at<kTok>(sm, p, id);
+      const uint32_t n = __shfl_sync(0xffffffffu, mma_n(t.rows), 0);
+      const uint32_t idesc0 = mxf4_idesc(n, 0);
+      if (!mbar_wait_warp(&sm.tmem_empty, acc_phase ^ 1u, p.err, &sm.abort_flag)) break;
+      tc_fence_after();
+      for (int kb = 0; kb < kb_n; ++kb) {
+        if (!mbar_wait_warp(&sm.full[stage], phase, p.err, &sm.abort_flag) ||
+            !mbar_wait_warp(&sm.full_sf[stage], phase, p.err, &sm.abort_flag)) {
+          ok = false;
+          break;
+        }
+        // The token scales land by cp.async (generic proxy): order them before
+        // the tensor core's (async proxy) reads.
+        fence_proxy_async_smem();
         tc_fence_after();
-        for (int kb = 0; kb < kb_n; ++kb) {
-          if (!mbar_wait(&sm.full[stage], phase, p.err, &sm.abort_flag) ||
-              !mbar_wait(&sm.full_sf[stage], phase, p.err, &sm.abort_flag)) {
-            ok = false;
-            break;
-          }
-          // The token scales land by cp.async (generic proxy): order them
-          // before the tensor core's (async proxy) reads.
-          fence_proxy_async_smem();
-          tc_fence_after();
-          const uint32_t sfw = tmem + kSfCol + set * kSfSet;
+        if (elect_one()) {
+          const uint32_t sfw = acc + kSfCol + set * kSfSet;
           const uint32_t sft = sfw + kSfTokens;
           const uint64_t sfwd = sfw_desc0 + static_cast<uint64_t>(stage) * (1024 >> 4);
           const uint64_t sftd =
@@ -338,22 +343,26 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks) {
             const uint32_t h = ks >> 1, sf_id = (ks & 1) * 2;
-            mma_mxf4(tmem, wd + ks * kKStep, td + ks * kKStep,
+            mma_mxf4(acc, wd + ks * kKStep, td + ks * kKStep,
                      idesc0 | (sf_id << 4) | (sf_id << 29), (sfw + 4 * h) | (sf_id << 30),
                      (sft + 8 * h) | (sf_id << 30), (kb > 0 || ks > 0) ? 1u : 0u);
           }
           tc_commit(&sm.empty[stage]);
-          set ^= 1u;
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
         }
-        if (!ok) break;
-        tc_commit(&sm.tmem_full);
-        acc_phase ^= 1u;
+        __syncwarp();
+        set ^= 1u;
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
-      // Everything issued above completes before the TMEM is freed.
+      if (!ok) break;
+      if (elect_one()) tc_commit(&sm.tmem_full);
+      __syncwarp();
+      acc_phase ^= 1u;
+    }
+    // Everything issued above completes before the TMEM is freed.
+    if (elect_one()) {
       tc_commit(&sm.drain);
       if (!mbar_wait_limited(&sm.drain, 0, kWaitLimitNs)) atomicOr(p.err, kErrTimeoutBit);
     }

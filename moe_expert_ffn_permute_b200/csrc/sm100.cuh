@@ -99,6 +99,29 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint32
   }
 }
 
+// The same wait by a whole warp: every lane polls, and the lanes agree on the
+// answer, so the code that follows stays warp-uniform.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, uint32_t* err,
+                                               volatile int* abort_flag) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, err, abort_flag));
+}
+
+// True on one lane of a converged warp.  A branch on elect.sync tells the
+// compiler that a single thread runs it, so operands that are warp-uniform
+// stay in uniform registers; under `lane == 0` every tensor-core and bulk-copy
+// instruction moves each of its operands there one by one, and an issuing
+// thread measured 58 clocks per tcgen05.cp and 72 per tcgen05.mma.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+
 // Wait with a time limit only (no abort flag): used on the way out of a
 // kernel, to let the tensor core finish before its TMEM is freed.
 __device__ __forceinline__ bool mbar_wait_limited(uint64_t* bar, uint32_t parity,
