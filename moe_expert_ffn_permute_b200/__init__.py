@@ -128,15 +128,28 @@ def _ptr(v):
     raise TypeError(f"expected an address or a tensor, got {type(v)}")
 
 
+_raw_stream = None
+
+
 def _stream(s):
     if s is None:
-        try:
-            import torch
-            if torch.cuda.is_available():
-                return torch.cuda.current_stream().cuda_stream
-        except ImportError:  # pragma: no cover
-            pass
-        return None
+        global _raw_stream
+        if _raw_stream is None:
+            try:
+                import torch
+            except ImportError:  # pragma: no cover
+                return None
+            if not torch.cuda.is_available():
+                return None
+            # The current stream's handle without a Stream object around it
+            # (0.3 us a call against 3.2 us for current_stream().cuda_stream).
+            device = torch.cuda.current_device
+            raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+            if raw is not None:
+                _raw_stream = lambda: raw(device())  # noqa: E731
+            else:  # pragma: no cover
+                _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+        return _raw_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -395,85 +408,88 @@ def _choice(fn, name, table, value):
                        f"{fn}: {name} must be one of {', '.join(table)}, got {value!r}") from None
 
 
-def _buffers(fn, *args):
-    """Addresses of a call's buffers, given as (name, tensor or address or None,
-    bytes the call reads or writes, torch dtype names it may have).  The C ABI
-    sees only pointers, so a tensor is checked here: contiguous, on the current
-    device, of the right type and long enough.  A raw address is passed through
-    (the caller vouches for it), and so is None (the library refuses it where it
-    is required)."""
-    device = None
-    out = []
-    for name, t, nbytes, dtypes in args:
-        if t is None or isinstance(t, int):
-            out.append(t)
-            continue
-        at = t.get_device()
-        if device is None:
-            import torch
-            device = torch.cuda.current_device() if at >= 0 else -2
-        if at != device:
-            raise MoEError(MOE_ERR_INVALID_ARG, f"{fn}: {name} must be on the current CUDA device, "
-                                                f"is on {t.device}")
-        if not t.is_contiguous():
-            raise MoEError(MOE_ERR_INVALID_ARG, f"{fn}: {name} must be contiguous")
-        if dtypes is not None and str(t.dtype)[6:] not in dtypes:
-            raise MoEError(MOE_ERR_INVALID_ARG,
-                           f"{fn}: {name} must be {' or '.join(dtypes)}, got {t.dtype}")
-        if t.numel() * t.element_size() < nbytes:
-            raise MoEError(MOE_ERR_INVALID_ARG,
-                           f"{fn}: {name} holds {t.numel() * t.element_size()} bytes, needs {nbytes}")
-        out.append(t.data_ptr())
-    return out
-
-
-_I32, _F32, _U8 = ("int32",), ("float32",), ("uint8",)
+_torch = None
+_I32, _F32, _U8, _ANY = ("int32",), ("float32",), ("uint8",), None
 _ELEM = {"bf16": (2, ("bfloat16",)), "fp16": (2, ("float16",)), "fp32": (4, ("float32",))}
+_DTYPE_NAMES = {}
+
+
+def _buf(fn, name, t, nbytes, dtypes):
+    """Address of one buffer of a call: a tensor, an address or None.  The C ABI
+    sees only pointers, so a tensor is checked here: contiguous, on the current
+    CUDA device, of one of `dtypes` (names; None: any) and at least `nbytes`
+    long.  A raw address is passed through (the caller vouches for it), and so
+    is None (the library refuses it where it is required)."""
+    if t is None or isinstance(t, int):
+        return t
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+        _DTYPE_NAMES.update({getattr(torch, n): n for n in ("int32", "float32", "uint8",
+                                                            "bfloat16", "float16")})
+    at = t.get_device()
+    if at < 0 or at != _torch.cuda.current_device():
+        raise MoEError(MOE_ERR_INVALID_ARG,
+                       f"{fn}: {name} must be on the current CUDA device, is on {t.device}")
+    if not t.is_contiguous():
+        raise MoEError(MOE_ERR_INVALID_ARG, f"{fn}: {name} must be contiguous")
+    if dtypes is not None and _DTYPE_NAMES.get(t.dtype) not in dtypes:
+        raise MoEError(MOE_ERR_INVALID_ARG,
+                       f"{fn}: {name} must be {' or '.join(dtypes)}, got {t.dtype}")
+    if t.nbytes < nbytes:
+        raise MoEError(MOE_ERR_INVALID_ARG, f"{fn}: {name} holds {t.nbytes} bytes, needs {nbytes}")
+    return t.data_ptr()
 
 
 def moe_permute(x, T, row_bytes, k, inv, rows, stream=None):
     """rows[inv[t, j]] = x[t]: x [T, row_bytes] of any type -> rows [T*k, row_bytes]."""
-    _sizes("moe_permute", T, k)
-    x, inv, rows = _buffers("moe_permute", ("x", x, T * row_bytes, None), ("inv", inv, 4 * T * k, _I32),
-                            ("rows", rows, T * k * row_bytes, None))
-    _check(lib().moe_permute(x, T, row_bytes, k, inv, rows, _stream(stream)), "moe_permute")
+    fn = "moe_permute"
+    _sizes(fn, T, k)
+    S = T * k
+    _check(lib().moe_permute(_buf(fn, "x", x, T * row_bytes, _ANY), T, row_bytes, k,
+                             _buf(fn, "inv", inv, 4 * S, _I32),
+                             _buf(fn, "rows", rows, S * row_bytes, _ANY), _stream(stream)), fn)
 
 
 def moe_permute_backward(drows, dtype, T, H, k, inv, dx, stream=None):
     """dx[t] = sum_j drows[inv[t, j]]; dtype "bf16", "fp16" or "fp32"."""
-    d = _choice("moe_permute_backward", "dtype", DTYPES, dtype)
-    _sizes("moe_permute_backward", T, H, k)
+    fn = "moe_permute_backward"
+    d = _choice(fn, "dtype", DTYPES, dtype)
+    _sizes(fn, T, H, k)
     z, tt = _ELEM[dtype]
-    drows, inv, dx = _buffers("moe_permute_backward", ("drows", drows, T * k * H * z, tt),
-                              ("inv", inv, 4 * T * k, _I32), ("dx", dx, T * H * z, tt))
-    _check(lib().moe_permute_backward(drows, d, T, H, k, inv, dx, _stream(stream)),
-           "moe_permute_backward")
+    S = T * k
+    _check(lib().moe_permute_backward(_buf(fn, "drows", drows, S * H * z, tt), d, T, H, k,
+                                      _buf(fn, "inv", inv, 4 * S, _I32),
+                                      _buf(fn, "dx", dx, T * H * z, tt), _stream(stream)), fn)
 
 
 def moe_unpermute(rows, dtype, T, H, k, inv, topk_w, out, stream=None):
     """out[t] = sum_j topk_w[t, j] * rows[inv[t, j]]; dtype "bf16", "fp16" or "fp32"."""
-    d = _choice("moe_unpermute", "dtype", DTYPES, dtype)
-    _sizes("moe_unpermute", T, H, k)
+    fn = "moe_unpermute"
+    d = _choice(fn, "dtype", DTYPES, dtype)
+    _sizes(fn, T, H, k)
     z, tt = _ELEM[dtype]
-    rows, inv, topk_w, out = _buffers(
-        "moe_unpermute", ("rows", rows, T * k * H * z, tt), ("inv", inv, 4 * T * k, _I32),
-        ("topk_w", topk_w, 4 * T * k, _F32), ("out", out, T * H * z, tt))
-    _check(lib().moe_unpermute(rows, d, T, H, k, inv, topk_w, out, _stream(stream)),
-           "moe_unpermute")
+    S = T * k
+    _check(lib().moe_unpermute(_buf(fn, "rows", rows, S * H * z, tt), d, T, H, k,
+                               _buf(fn, "inv", inv, 4 * S, _I32),
+                               _buf(fn, "topk_w", topk_w, 4 * S, _F32),
+                               _buf(fn, "out", out, T * H * z, tt), _stream(stream)), fn)
 
 
 def moe_unpermute_backward(dout, rows, dtype, T, H, k, inv, topk_w, drows, dw, stream=None):
     """drows[inv[t, j]] = topk_w[t, j] * dout[t]; dw[t, j] = <dout[t], rows[inv[t, j]]>.
     drows or dw may be None; rows too when dw is."""
-    d = _choice("moe_unpermute_backward", "dtype", DTYPES, dtype)
-    _sizes("moe_unpermute_backward", T, H, k)
+    fn = "moe_unpermute_backward"
+    d = _choice(fn, "dtype", DTYPES, dtype)
+    _sizes(fn, T, H, k)
     z, tt = _ELEM[dtype]
-    args = _buffers("moe_unpermute_backward", ("dout", dout, T * H * z, tt),
-                    ("rows", rows, T * k * H * z, tt), ("inv", inv, 4 * T * k, _I32),
-                    ("topk_w", topk_w, 4 * T * k, _F32), ("drows", drows, T * k * H * z, tt),
-                    ("dw", dw, 4 * T * k, _F32))
-    _check(lib().moe_unpermute_backward(args[0], args[1], d, T, H, k, *args[2:], _stream(stream)),
-           "moe_unpermute_backward")
+    S = T * k
+    _check(lib().moe_unpermute_backward(
+        _buf(fn, "dout", dout, T * H * z, tt), _buf(fn, "rows", rows, S * H * z, tt), d, T, H, k,
+        _buf(fn, "inv", inv, 4 * S, _I32), _buf(fn, "topk_w", topk_w, 4 * S, _F32),
+        _buf(fn, "drows", drows, S * H * z, tt), _buf(fn, "dw", dw, 4 * S, _F32),
+        _stream(stream)), fn)
 
 
 def mxfp4_scale_shape(R, K, layout):
@@ -481,34 +497,36 @@ def mxfp4_scale_shape(R, K, layout):
     return (R, K // 32) if layout == "row" else ((K + 127) // 128, R, 4)
 
 
+def _scale_bytes(R, K, layout):
+    return R * (K // 32) if layout == 0 else (K + 127) // 128 * R * 4
+
+
 def moe_quantize_mxfp4(x, dtype, T, K, k, inv, codes, scales, scale_layout="row", stream=None):
     """x [T, K] -> E2M1 codes u8 [T*k, K/2] and UE8M0 scales (mxfp4_scale_shape), each
     token's row at the positions of its slots; inv None (k = 1): in order."""
-    d = _choice("moe_quantize_mxfp4", "dtype", DTYPES, dtype)
-    s = _choice("moe_quantize_mxfp4", "scale_layout", SCALE_LAYOUTS, scale_layout)
-    _sizes("moe_quantize_mxfp4", T, K, k)
+    fn = "moe_quantize_mxfp4"
+    d = _choice(fn, "dtype", DTYPES, dtype)
+    s = _choice(fn, "scale_layout", SCALE_LAYOUTS, scale_layout)
+    _sizes(fn, T, K, k)
     z, tt = _ELEM[dtype]
     R = T * k
-    nscale = R * (K // 32) if s == 0 else (K + 127) // 128 * R * 4
-    x, inv, codes, scales = _buffers(
-        "moe_quantize_mxfp4", ("x", x, T * K * z, tt), ("inv", inv, 4 * R, _I32),
-        ("codes", codes, R * (K // 2), _U8), ("scales", scales, nscale, _U8))
-    _check(lib().moe_quantize_mxfp4(x, d, T, K, k, inv, codes, scales, s, _stream(stream)),
-           "moe_quantize_mxfp4")
+    _check(lib().moe_quantize_mxfp4(
+        _buf(fn, "x", x, T * K * z, tt), d, T, K, k, _buf(fn, "inv", inv, 4 * R, _I32),
+        _buf(fn, "codes", codes, R * (K // 2), _U8),
+        _buf(fn, "scales", scales, _scale_bytes(R, K, s), _U8), s, _stream(stream)), fn)
 
 
 def moe_dequantize_mxfp4(codes, scales, scale_layout, R, K, dtype, out, stream=None):
     """The values of codes u8 [R, K/2] and their scales -> out [R, K]."""
-    d = _choice("moe_dequantize_mxfp4", "dtype", DTYPES, dtype)
-    s = _choice("moe_dequantize_mxfp4", "scale_layout", SCALE_LAYOUTS, scale_layout)
-    _sizes("moe_dequantize_mxfp4", R, K)
+    fn = "moe_dequantize_mxfp4"
+    d = _choice(fn, "dtype", DTYPES, dtype)
+    s = _choice(fn, "scale_layout", SCALE_LAYOUTS, scale_layout)
+    _sizes(fn, R, K)
     z, tt = _ELEM[dtype]
-    nscale = R * (K // 32) if s == 0 else (K + 127) // 128 * R * 4
-    codes, scales, out = _buffers(
-        "moe_dequantize_mxfp4", ("codes", codes, R * (K // 2), _U8), ("scales", scales, nscale, _U8),
-        ("out", out, R * K * z, tt))
-    _check(lib().moe_dequantize_mxfp4(codes, scales, s, R, K, d, out, _stream(stream)),
-           "moe_dequantize_mxfp4")
+    _check(lib().moe_dequantize_mxfp4(
+        _buf(fn, "codes", codes, R * (K // 2), _U8),
+        _buf(fn, "scales", scales, _scale_bytes(R, K, s), _U8), s, R, K, d,
+        _buf(fn, "out", out, R * K * z, tt), _stream(stream)), fn)
 
 
 def moe_mxfp4_weight_bytes(E, N, K):
@@ -524,17 +542,16 @@ def moe_mxfp4_weight_scale_bytes(E, N, K):
 
 def moe_mxfp4_prepack(w, w_scales, E, N, K, w_tiled, w_scales_chunked, stream=None):
     """Weights u8 [E, N, K/2] and scales u8 [E, N, K/32] -> the layout moe_mxfp4_gemm reads."""
-    _sizes("moe_mxfp4_prepack", E, N, K)
-    w, w_scales, w_tiled, w_scales_chunked = _buffers(
-        "moe_mxfp4_prepack", ("w", w, E * N * (K // 2), _U8),
-        ("w_scales", w_scales, E * N * (K // 32), _U8),
-        ("w_tiled", w_tiled, moe_mxfp4_weight_bytes(E, N, K), _U8),
-        ("w_scales_chunked", w_scales_chunked, moe_mxfp4_weight_scale_bytes(E, N, K), _U8))
-    _check(lib().moe_mxfp4_prepack(w, w_scales, E, N, K, w_tiled, w_scales_chunked,
-                                   _stream(stream)), "moe_mxfp4_prepack")
+    fn = "moe_mxfp4_prepack"
+    wb, sb = moe_mxfp4_weight_bytes(E, N, K), moe_mxfp4_weight_scale_bytes(E, N, K)
+    _check(lib().moe_mxfp4_prepack(
+        _buf(fn, "w", w, E * N * (K // 2), _U8), _buf(fn, "w_scales", w_scales, E * N * (K // 32), _U8),
+        E, N, K, _buf(fn, "w_tiled", w_tiled, wb, _U8),
+        _buf(fn, "w_scales_chunked", w_scales_chunked, sb, _U8), _stream(stream)), fn)
 
 
 def moe_mxfp4_workspace_bytes(R, E, N, K):
+    """Bytes of moe_mxfp4_gemm's workspace on the current device (0: sizes it does not take)."""
     _sizes("moe_mxfp4_workspace_bytes", R, E, N, K)
     return lib().moe_mxfp4_workspace_bytes(R, E, N, K)
 
@@ -544,19 +561,20 @@ def moe_mxfp4_gemm(codes, scales, offsets, R, E, N, K, w_tiled, w_scales_chunked
     """out[r] = a[r] @ w[e]^T for the rows r of expert e (offsets i32 [E+1]; None: one
     group): codes u8 [R, K/2] with group-major scales, prepacked weights, out [R, N]
     "bf16" or "fp16".  workspace: moe_mxfp4_workspace_bytes, zeroed before its first use."""
-    d = _choice("moe_mxfp4_gemm", "dtype", DTYPES, dtype)
-    _sizes("moe_mxfp4_gemm", R, E, N, K)
+    fn = "moe_mxfp4_gemm"
+    d = _choice(fn, "dtype", DTYPES, dtype)
+    _sizes(fn, R, E, N, K)
     L = lib()
     z, tt = _ELEM[dtype]
-    p = _buffers("moe_mxfp4_gemm", ("codes", codes, R * (K // 2), _U8),
-                 ("scales", scales, (K + 127) // 128 * R * 4, _U8),
-                 ("offsets", offsets, 4 * (E + 1), _I32),
-                 ("w_tiled", w_tiled, L.moe_mxfp4_weight_bytes(E, N, K), _U8),
-                 ("w_scales_chunked", w_scales_chunked, L.moe_mxfp4_weight_scale_bytes(E, N, K), _U8),
-                 ("out", out, R * N * z, tt),
-                 ("workspace", workspace, L.moe_mxfp4_workspace_bytes(R, E, N, K), None))
-    _check(L.moe_mxfp4_gemm(p[0], p[1], p[2], R, E, N, K, p[3], p[4], d, p[5], p[6],
-                            _stream(stream)), "moe_mxfp4_gemm")
+    _check(L.moe_mxfp4_gemm(
+        _buf(fn, "codes", codes, R * (K // 2), _U8),
+        _buf(fn, "scales", scales, _scale_bytes(R, K, 1), _U8),
+        _buf(fn, "offsets", offsets, 4 * (E + 1), _I32), R, E, N, K,
+        _buf(fn, "w_tiled", w_tiled, L.moe_mxfp4_weight_bytes(E, N, K), _U8),
+        _buf(fn, "w_scales_chunked", w_scales_chunked, L.moe_mxfp4_weight_scale_bytes(E, N, K), _U8),
+        d, _buf(fn, "out", out, R * N * z, tt),
+        _buf(fn, "workspace", workspace, L.moe_mxfp4_workspace_bytes(R, E, N, K), _ANY),
+        _stream(stream)), fn)
 
 
 def moe_mxfp4_clear_error(workspace, stream=None):
