@@ -380,8 +380,9 @@ moe_status moe_mxfp4_prepack(const uint8_t *w, const uint8_t *w_scales, int E, i
                              uint8_t *w_tiled, uint8_t *w_scales_chunked, moe_stream_t stream);
 
 /* Bytes of moe_mxfp4_gemm's workspace (device, 256-byte aligned); 0 for sizes it
- * does not take.  Zero the workspace once before its first use; calls leave it
- * ready for the next.  Calls that may overlap on the GPU need workspaces of
+ * does not take; for the current device.  Zero the workspace once before its
+ * first use; calls leave it ready for the next (of the same or other sizes that
+ * it is large enough for).  Calls that may overlap on the GPU need workspaces of
  * their own.
  * No counterpart on the pages.
  */
@@ -405,8 +406,9 @@ moe_status moe_mxfp4_gemm(const uint8_t *codes, const uint8_t *scales, const int
                           const uint8_t *w_scales_chunked, int dtype, void *out,
                           void *workspace, moe_stream_t stream);
 
-/* Zero the workspace's error word (enqueued on `stream`), and read it: the
- * latter synchronises `stream` and returns MOE_OK or MOE_ERR_DEVICE_TIMEOUT.
+/* Make the workspace ready again after a device-side error (enqueued on
+ * `stream`), and read its error word: the latter synchronises `stream` and
+ * returns MOE_OK or MOE_ERR_DEVICE_TIMEOUT.
  * No counterpart on the pages.
  */
 moe_status moe_mxfp4_clear_error(void *workspace, moe_stream_t stream);

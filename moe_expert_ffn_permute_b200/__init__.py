@@ -408,48 +408,55 @@ def _choice(fn, name, table, value):
                        f"{fn}: {name} must be one of {', '.join(table)}, got {value!r}") from None
 
 
-_torch = None
-_I32, _F32, _U8, _ANY = ("int32",), ("float32",), ("uint8",), None
-_ELEM = {"bf16": (2, ("bfloat16",)), "fp16": (2, ("float16",)), "fp32": (4, ("float32",))}
-_DTYPE_NAMES = {}
+_ELEM = {"bf16": 2, "fp16": 2, "fp32": 4}     # bytes per element
+_current_device = None
+_TYPE = {}                                     # name -> torch dtype
 
 
-def _buf(fn, name, t, nbytes, dtypes):
+def _device():
+    """The current CUDA device's index (-2 without CUDA: no tensor is on it)."""
+    global _current_device
+    if _current_device is None:
+        import torch
+        _TYPE.update(i32=torch.int32, f32=torch.float32, u8=torch.uint8, bf16=torch.bfloat16,
+                     fp16=torch.float16, fp32=torch.float32, any=None)
+        if not torch.cuda.is_available():
+            return -2
+        _current_device = torch.cuda.current_device
+    return _current_device()
+
+
+def _buf(fn, name, t, nbytes, dtype, device):
     """Address of one buffer of a call: a tensor, an address or None.  The C ABI
     sees only pointers, so a tensor is checked here: contiguous, on the current
-    CUDA device, of one of `dtypes` (names; None: any) and at least `nbytes`
-    long.  A raw address is passed through (the caller vouches for it), and so
-    is None (the library refuses it where it is required)."""
+    CUDA device (`device`, from _device()), of type `dtype` (a key of _TYPE) and
+    at least `nbytes` long.  A raw address is passed through (the caller vouches
+    for it), and so is None (the library refuses it where it is required)."""
     if t is None or isinstance(t, int):
         return t
-    global _torch
-    if _torch is None:
-        import torch
-        _torch = torch
-        _DTYPE_NAMES.update({getattr(torch, n): n for n in ("int32", "float32", "uint8",
-                                                            "bfloat16", "float16")})
-    at = t.get_device()
-    if at < 0 or at != _torch.cuda.current_device():
-        raise MoEError(MOE_ERR_INVALID_ARG,
-                       f"{fn}: {name} must be on the current CUDA device, is on {t.device}")
-    if not t.is_contiguous():
-        raise MoEError(MOE_ERR_INVALID_ARG, f"{fn}: {name} must be contiguous")
-    if dtypes is not None and _DTYPE_NAMES.get(t.dtype) not in dtypes:
-        raise MoEError(MOE_ERR_INVALID_ARG,
-                       f"{fn}: {name} must be {' or '.join(dtypes)}, got {t.dtype}")
-    if t.nbytes < nbytes:
-        raise MoEError(MOE_ERR_INVALID_ARG, f"{fn}: {name} holds {t.nbytes} bytes, needs {nbytes}")
-    return t.data_ptr()
+    want = _TYPE[dtype]
+    if (t.get_device() == device and t.is_contiguous() and (want is None or t.dtype is want)
+            and t.nbytes >= nbytes):
+        return t.data_ptr()
+    if t.get_device() != device:
+        what = f"must be on the current CUDA device, is on {t.device}"
+    elif not t.is_contiguous():
+        what = "must be contiguous"
+    elif want is not None and t.dtype is not want:
+        what = f"must be {want}, got {t.dtype}"
+    else:
+        what = f"holds {t.nbytes} bytes, needs {nbytes}"
+    raise MoEError(MOE_ERR_INVALID_ARG, f"{fn}: {name} {what}")
 
 
 def moe_permute(x, T, row_bytes, k, inv, rows, stream=None):
     """rows[inv[t, j]] = x[t]: x [T, row_bytes] of any type -> rows [T*k, row_bytes]."""
     fn = "moe_permute"
     _sizes(fn, T, k)
-    S = T * k
-    _check(lib().moe_permute(_buf(fn, "x", x, T * row_bytes, _ANY), T, row_bytes, k,
-                             _buf(fn, "inv", inv, 4 * S, _I32),
-                             _buf(fn, "rows", rows, S * row_bytes, _ANY), _stream(stream)), fn)
+    S, at = T * k, _device()
+    _check(lib().moe_permute(_buf(fn, "x", x, T * row_bytes, "any", at), T, row_bytes, k,
+                             _buf(fn, "inv", inv, 4 * S, "i32", at),
+                             _buf(fn, "rows", rows, S * row_bytes, "any", at), _stream(stream)), fn)
 
 
 def moe_permute_backward(drows, dtype, T, H, k, inv, dx, stream=None):
@@ -457,11 +464,11 @@ def moe_permute_backward(drows, dtype, T, H, k, inv, dx, stream=None):
     fn = "moe_permute_backward"
     d = _choice(fn, "dtype", DTYPES, dtype)
     _sizes(fn, T, H, k)
-    z, tt = _ELEM[dtype]
+    z, at = _ELEM[dtype], _device()
     S = T * k
-    _check(lib().moe_permute_backward(_buf(fn, "drows", drows, S * H * z, tt), d, T, H, k,
-                                      _buf(fn, "inv", inv, 4 * S, _I32),
-                                      _buf(fn, "dx", dx, T * H * z, tt), _stream(stream)), fn)
+    _check(lib().moe_permute_backward(_buf(fn, "drows", drows, S * H * z, dtype, at), d, T, H, k,
+                                      _buf(fn, "inv", inv, 4 * S, "i32", at),
+                                      _buf(fn, "dx", dx, T * H * z, dtype, at), _stream(stream)), fn)
 
 
 def moe_unpermute(rows, dtype, T, H, k, inv, topk_w, out, stream=None):
@@ -469,12 +476,12 @@ def moe_unpermute(rows, dtype, T, H, k, inv, topk_w, out, stream=None):
     fn = "moe_unpermute"
     d = _choice(fn, "dtype", DTYPES, dtype)
     _sizes(fn, T, H, k)
-    z, tt = _ELEM[dtype]
+    z, at = _ELEM[dtype], _device()
     S = T * k
-    _check(lib().moe_unpermute(_buf(fn, "rows", rows, S * H * z, tt), d, T, H, k,
-                               _buf(fn, "inv", inv, 4 * S, _I32),
-                               _buf(fn, "topk_w", topk_w, 4 * S, _F32),
-                               _buf(fn, "out", out, T * H * z, tt), _stream(stream)), fn)
+    _check(lib().moe_unpermute(_buf(fn, "rows", rows, S * H * z, dtype, at), d, T, H, k,
+                               _buf(fn, "inv", inv, 4 * S, "i32", at),
+                               _buf(fn, "topk_w", topk_w, 4 * S, "f32", at),
+                               _buf(fn, "out", out, T * H * z, dtype, at), _stream(stream)), fn)
 
 
 def moe_unpermute_backward(dout, rows, dtype, T, H, k, inv, topk_w, drows, dw, stream=None):
@@ -483,12 +490,12 @@ def moe_unpermute_backward(dout, rows, dtype, T, H, k, inv, topk_w, drows, dw, s
     fn = "moe_unpermute_backward"
     d = _choice(fn, "dtype", DTYPES, dtype)
     _sizes(fn, T, H, k)
-    z, tt = _ELEM[dtype]
+    z, at = _ELEM[dtype], _device()
     S = T * k
     _check(lib().moe_unpermute_backward(
-        _buf(fn, "dout", dout, T * H * z, tt), _buf(fn, "rows", rows, S * H * z, tt), d, T, H, k,
-        _buf(fn, "inv", inv, 4 * S, _I32), _buf(fn, "topk_w", topk_w, 4 * S, _F32),
-        _buf(fn, "drows", drows, S * H * z, tt), _buf(fn, "dw", dw, 4 * S, _F32),
+        _buf(fn, "dout", dout, T * H * z, dtype, at), _buf(fn, "rows", rows, S * H * z, dtype, at), d, T, H, k,
+        _buf(fn, "inv", inv, 4 * S, "i32", at), _buf(fn, "topk_w", topk_w, 4 * S, "f32", at),
+        _buf(fn, "drows", drows, S * H * z, dtype, at), _buf(fn, "dw", dw, 4 * S, "f32", at),
         _stream(stream)), fn)
 
 
@@ -508,12 +515,12 @@ def moe_quantize_mxfp4(x, dtype, T, K, k, inv, codes, scales, scale_layout="row"
     d = _choice(fn, "dtype", DTYPES, dtype)
     s = _choice(fn, "scale_layout", SCALE_LAYOUTS, scale_layout)
     _sizes(fn, T, K, k)
-    z, tt = _ELEM[dtype]
+    z, at = _ELEM[dtype], _device()
     R = T * k
     _check(lib().moe_quantize_mxfp4(
-        _buf(fn, "x", x, T * K * z, tt), d, T, K, k, _buf(fn, "inv", inv, 4 * R, _I32),
-        _buf(fn, "codes", codes, R * (K // 2), _U8),
-        _buf(fn, "scales", scales, _scale_bytes(R, K, s), _U8), s, _stream(stream)), fn)
+        _buf(fn, "x", x, T * K * z, dtype, at), d, T, K, k, _buf(fn, "inv", inv, 4 * R, "i32", at),
+        _buf(fn, "codes", codes, R * (K // 2), "u8", at),
+        _buf(fn, "scales", scales, _scale_bytes(R, K, s), "u8", at), s, _stream(stream)), fn)
 
 
 def moe_dequantize_mxfp4(codes, scales, scale_layout, R, K, dtype, out, stream=None):
@@ -522,11 +529,16 @@ def moe_dequantize_mxfp4(codes, scales, scale_layout, R, K, dtype, out, stream=N
     d = _choice(fn, "dtype", DTYPES, dtype)
     s = _choice(fn, "scale_layout", SCALE_LAYOUTS, scale_layout)
     _sizes(fn, R, K)
-    z, tt = _ELEM[dtype]
+    z, at = _ELEM[dtype], _device()
     _check(lib().moe_dequantize_mxfp4(
-        _buf(fn, "codes", codes, R * (K // 2), _U8),
-        _buf(fn, "scales", scales, _scale_bytes(R, K, s), _U8), s, R, K, d,
-        _buf(fn, "out", out, R * K * z, tt), _stream(stream)), fn)
+        _buf(fn, "codes", codes, R * (K // 2), "u8", at),
+        _buf(fn, "scales", scales, _scale_bytes(R, K, s), "u8", at), s, R, K, d,
+        _buf(fn, "out", out, R * K * z, dtype, at), _stream(stream)), fn)
+
+
+def _weight_tiles(E, N, K):
+    """Tiles of prepacked weights (the library refuses sizes it does not take itself)."""
+    return E * -(-N // 128) * -(-K // 256)
 
 
 def moe_mxfp4_weight_bytes(E, N, K):
@@ -543,11 +555,12 @@ def moe_mxfp4_weight_scale_bytes(E, N, K):
 def moe_mxfp4_prepack(w, w_scales, E, N, K, w_tiled, w_scales_chunked, stream=None):
     """Weights u8 [E, N, K/2] and scales u8 [E, N, K/32] -> the layout moe_mxfp4_gemm reads."""
     fn = "moe_mxfp4_prepack"
-    wb, sb = moe_mxfp4_weight_bytes(E, N, K), moe_mxfp4_weight_scale_bytes(E, N, K)
+    _sizes(fn, E, N, K)
+    tiles, at = _weight_tiles(E, N, K), _device()
     _check(lib().moe_mxfp4_prepack(
-        _buf(fn, "w", w, E * N * (K // 2), _U8), _buf(fn, "w_scales", w_scales, E * N * (K // 32), _U8),
-        E, N, K, _buf(fn, "w_tiled", w_tiled, wb, _U8),
-        _buf(fn, "w_scales_chunked", w_scales_chunked, sb, _U8), _stream(stream)), fn)
+        _buf(fn, "w", w, E * N * (K // 2), "u8", at), _buf(fn, "w_scales", w_scales, E * N * (K // 32), "u8", at),
+        E, N, K, _buf(fn, "w_tiled", w_tiled, tiles * 16384, "u8", at),
+        _buf(fn, "w_scales_chunked", w_scales_chunked, tiles * 1024, "u8", at), _stream(stream)), fn)
 
 
 def moe_mxfp4_workspace_bytes(R, E, N, K):
@@ -564,16 +577,15 @@ def moe_mxfp4_gemm(codes, scales, offsets, R, E, N, K, w_tiled, w_scales_chunked
     fn = "moe_mxfp4_gemm"
     d = _choice(fn, "dtype", DTYPES, dtype)
     _sizes(fn, R, E, N, K)
-    L = lib()
-    z, tt = _ELEM[dtype]
-    _check(L.moe_mxfp4_gemm(
-        _buf(fn, "codes", codes, R * (K // 2), _U8),
-        _buf(fn, "scales", scales, _scale_bytes(R, K, 1), _U8),
-        _buf(fn, "offsets", offsets, 4 * (E + 1), _I32), R, E, N, K,
-        _buf(fn, "w_tiled", w_tiled, L.moe_mxfp4_weight_bytes(E, N, K), _U8),
-        _buf(fn, "w_scales_chunked", w_scales_chunked, L.moe_mxfp4_weight_scale_bytes(E, N, K), _U8),
-        d, _buf(fn, "out", out, R * N * z, tt),
-        _buf(fn, "workspace", workspace, L.moe_mxfp4_workspace_bytes(R, E, N, K), _ANY),
+    z, at = _ELEM[dtype], _device()
+    tiles = _weight_tiles(E, N, K)
+    _check(lib().moe_mxfp4_gemm(
+        _buf(fn, "codes", codes, R * (K // 2), "u8", at),
+        _buf(fn, "scales", scales, _scale_bytes(R, K, 1), "u8", at),
+        _buf(fn, "offsets", offsets, 4 * (E + 1), "i32", at), R, E, N, K,
+        _buf(fn, "w_tiled", w_tiled, tiles * 16384, "u8", at),
+        _buf(fn, "w_scales_chunked", w_scales_chunked, tiles * 1024, "u8", at), d,
+        _buf(fn, "out", out, R * N * z, dtype, at), _buf(fn, "workspace", workspace, 256, "any", at),
         _stream(stream)), fn)
 
 

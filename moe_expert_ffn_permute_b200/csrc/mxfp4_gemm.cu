@@ -74,25 +74,19 @@ struct __align__(1024) Smem {
 
 struct Params {
   int R, E, N, K;
+  int cap;                    // most tokens of a tile (a multiple of 16, at most kTok)
   int nb_n, kb_n;             // 128-row weight blocks, 256-wide K blocks
   const int32_t* offsets;     // null: one group of all rows
   const uint8_t* w;           // prepacked tiles
   const uint8_t* w_sf;        // prepacked scale chunks
   const uint8_t* scales;      // token scales, group-major [ceil(K/128)][R][4]
   uint16_t* out;
-  int fp16;
   uint32_t* err;
 };
 
 struct Tile {
-  int e, nb, row, rows;       // expert, weight block, first row, rows (1..kTok)
+  int e, nb, row, rows;       // expert, weight block, first row, rows (1..cap)
 };
-
-// Token tiles of a group of n rows.
-template <int kTok>
-__device__ __forceinline__ int tiles_of(int n) {
-  return (n + kTok - 1) / kTok;
-}
 
 // Tile `id` of the launch: the groups' token tiles in order, each with all its
 // weight blocks.  A group is cut into tiles of equal size (a multiple of 16).
@@ -119,20 +113,33 @@ __device__ __forceinline__ Tile tile_at(const Smem<kTok>& sm, const Params& p, l
   return t;
 }
 
+// The value on lane 0: the same on every lane, and the compiler knows it.
+template <class T>
+__device__ __forceinline__ T uniform(T v) {
+  return __shfl_sync(0xffffffffu, v, 0);
+}
+
 __device__ __forceinline__ uint32_t mma_n(int rows) {
   return static_cast<uint32_t>((rows + 15) & ~15);
 }
 
-__device__ __forceinline__ uint32_t pack_out(float lo, float hi, bool fp16) {
-  uint32_t r;
-  if (fp16)
+// Two fp32 -> two 16-bit floats, round to nearest even; `lo` in the low half.
+template <bool kFp16>
+__device__ __forceinline__ uint32_t pack_out(float lo, float hi) {
+  if constexpr (kFp16) {
+    uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  else
-    r = pack_bf16x2(lo, hi);
-  return r;
+    return r;
+  } else {
+    return pack_bf16x2(lo, hi);
+  }
 }
 
-template <int kTok>
+// Token columns [c0, c0 + cols) of an accumulator of n columns are half h's: the
+// two warps of a sub-partition share a tile's tokens evenly.
+__device__ __forceinline__ int half_begin(int n, int h) { return h ? (n / 2 + 7) & ~7 : 0; }
+
+template <int kTok, bool kFp16>
 __global__ void __launch_bounds__(kThreads, 1)
     mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap, const Params p) {
   using C = Cfg<kTok>;
@@ -142,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Smem<kTok>& sm = *reinterpret_cast<Smem<kTok>*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   // (The shuffle makes the warp's number uniform to the compiler.)
-  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
+  const int warp = uniform(static_cast<int>(threadIdx.x >> 5));
   const int lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -192,7 +199,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int carry = 0;
     for (int b = 0; b < p.E; b += 32) {
       const int i = b + lane;
-      const int own = i < p.E ? tiles_of<kTok>(sm.row_off[i + 1] - sm.row_off[i]) : 0;
+      const int rows = i < p.E ? sm.row_off[i + 1] - sm.row_off[i] : 0;
+      const int own = (rows + p.cap - 1) / p.cap;
       int v = own;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -208,8 +216,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
-  const long long tiles = static_cast<long long>(sm.tile_off[p.E]) * p.nb_n;
   const int kb_n = p.kb_n;
+  const long long tiles = static_cast<long long>(sm.tile_off[p.E]) * p.nb_n;
+  const int my_tiles = uniform(
+      static_cast<int>((tiles - blockIdx.x + gridDim.x - 1) / gridDim.x));   // may be <= 0
 
   // The issuing warps run warp-uniform loops and elect a lane for the copies and
   // MMAs alone (elect_one() says what that saves).
@@ -222,13 +232,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t phase = 0;
     long long issued = 0;   // stages filled
     bool ok = true;
-    for (long long id = blockIdx.x; ok && id < tiles; id += gridDim.x) {
-      const Tile t = tile_at<kTok>(sm, p, id);
+    for (int i = 0; ok && i < my_tiles; ++i) {
+      const Tile t = tile_at<kTok>(sm, p, blockIdx.x + static_cast<long long>(i) * gridDim.x);
       // Weights of an expert with one token tile are read once.
       const uint64_t pol_w = sm.tile_off[t.e + 1] - sm.tile_off[t.e] > 1 ? pol_reused : pol_once;
-      const int boxes = (t.rows + C::kBox - 1) / C::kBox;
+      const int boxes = uniform((t.rows + C::kBox - 1) / C::kBox);
       const uint32_t bytes = kTileBytes + 1024 + boxes * C::kBox * kKBytes;
-      const size_t block = (static_cast<size_t>(t.e) * p.nb_n + t.nb) * kb_n;
+      const long long block = uniform((static_cast<long long>(t.e) * p.nb_n + t.nb) * kb_n);
+      const int row = uniform(t.row);
       for (int kb = 0; kb < kb_n; ++kb) {
         if (!mbar_wait_warp(&sm.empty[stage], phase ^ 1u, p.err, &sm.abort_flag)) {
           ok = false;
@@ -241,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           bulk_load_hint(sm.sfw[stage], p.w_sf + (block + kb) * 1024, 1024, &sm.full[stage], pol_w);
           for (int b = 0; b < boxes; ++b)
             tma_load_2d(sm.t[stage] + b * C::kBox * kKBytes, &tmap, kb * kKBytes,
-                        t.row + b * C::kBox, &sm.full[stage], pol_tok);
+                        row + b * C::kBox, &sm.full[stage], pol_tok);
         }
         __syncwarp();
         ++issued;
@@ -268,8 +279,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (long long id = blockIdx.x; ok && id < tiles; id += gridDim.x) {
-      const Tile t = tile_at<kTok>(sm, p, id);
+    for (int i = 0; ok && i < my_tiles; ++i) {
+      const Tile t = tile_at<kTok>(sm, p, blockIdx.x + static_cast<long long>(i) * gridDim.x);
       const int quads = (t.rows + 31) / 32;
       for (int kb = 0; kb < kb_n; ++kb) {
         if (!mbar_wait(&sm.empty[stage], phase ^ 1u, p.err, &sm.abort_flag)) {
@@ -300,16 +311,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ MMA issue
     int stage = 0;
     uint32_t phase = 0, acc_phase = 0, set = 0;
-    const uint32_t acc = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint32_t acc = uniform(tmem);
     const uint64_t w_desc0 = umma_desc_sw128(smem_u32(sm.w[0]));
     const uint64_t t_desc0 = umma_desc_sw128(smem_u32(sm.t[0]));
     const uint64_t sfw_desc0 = sf_desc(smem_u32(sm.sfw[0]));
     const uint64_t sft_desc0 = sf_desc(smem_u32(sm.sft[0]));
     constexpr uint64_t kKStep = 32 >> 4, kSfChunk = 512 >> 4;
     bool ok = true;
-    for (long long id = blockIdx.x; ok && id < tiles; id += gridDim.x) {
-      const Tile t = tile_at<kTok>(sm, p, id);
-      const uint32_t n = __shfl_sync(0xffffffffu, mma_n(t.rows), 0);
+    for (int i = 0; ok && i < my_tiles; ++i) {
+      const Tile t = tile_at<kTok>(sm, p, blockIdx.x + static_cast<long long>(i) * gridDim.x);
+      const uint32_t n = uniform(mma_n(t.rows));
       const uint32_t idesc0 = mxf4_idesc(n, 0);
       if (!mbar_wait_warp(&sm.tmem_empty, acc_phase ^ 1u, p.err, &sm.abort_flag)) break;
       tc_fence_after();
@@ -372,38 +383,46 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q = warp & 3;              // TMEM sub-partition: lanes 32q..32q+31
     const int half = (warp - 4) >> 2;    // which half of the tile's token columns
     constexpr int kCols = kTok / 2;
-    const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * kCols;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    const bool odd = lane & 1;
+    const uint32_t pick = odd ? 0x3276u : 0x5410u;
     uint32_t acc_phase = 0;
-    for (long long id = blockIdx.x; id < tiles; id += gridDim.x) {
-      const Tile t = tile_at<kTok>(sm, p, id);
+    for (int i = 0; i < my_tiles; ++i) {
+      const Tile t = tile_at<kTok>(sm, p, blockIdx.x + static_cast<long long>(i) * gridDim.x);
+      const int n = static_cast<int>(mma_n(t.rows));
+      const int c0 = half_begin(n, half), cols = half ? n - c0 : half_begin(n, 1);
       if (!mbar_wait(&sm.tmem_full, acc_phase, p.err, &sm.abort_flag)) break;
       acc_phase ^= 1u;
       tc_fence_after();
-      // (All columns are loaded whatever the tile holds: they are always
+      // (kCols columns are loaded whatever the tile holds: they are always
       // addressable, and a conditional load would put the array in local
       // memory.)
       uint32_t v[kCols];
 #pragma unroll
       for (int c = 0; c < kCols / 32; ++c)
-        tmem_ld_32x32b_x32(taddr + c * 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32 * c));
+        tmem_ld_32x32b_x32(lanes + c0 + c * 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32 * c));
       tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.tmem_empty);
-      // Lane = feature, register = token.  Neighbouring lanes trade tokens of a
-      // pair so that an even lane holds two features of the first and an odd
-      // lane of the second: 4-byte stores, 64 contiguous bytes per token.
-      const bool odd = lane & 1;
+      // Lane = feature, register = token.  Neighbouring lanes trade halves of a
+      // pair of tokens so that an even lane holds two features of the first and
+      // an odd lane of the second: 4-byte stores, 64 contiguous bytes per token.
       const int f = t.nb * 128 + q * 32 + (lane & ~1);
-      const int j0 = half * kCols;
-      uint16_t* dst = p.out + (static_cast<size_t>(t.row) + j0 + (odd ? 1 : 0)) * p.N + f;
-      const int left = f < p.N ? t.rows - j0 - (odd ? 1 : 0) : 0;   // tokens from j0 (+ 1) on
+      uint16_t* dst = p.out + (static_cast<size_t>(t.row) + c0 + (odd ? 1 : 0)) * p.N + f;
+      const size_t step = 2 * static_cast<size_t>(p.N);
+      // Tokens of this half, counted from the lane's first.
+      const int left = f < p.N ? min(cols, t.rows - c0) - (odd ? 1 : 0) : 0;
 #pragma unroll
-      for (int j = 0; j < kCols; j += 2) {
-        const float a = __uint_as_float(v[j]), b = __uint_as_float(v[j + 1]);
-        const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
-        const uint32_t w = odd ? pack_out(got, b, p.fp16) : pack_out(a, got, p.fp16);
-        if (j < left) *reinterpret_cast<uint32_t*>(dst + static_cast<size_t>(j) * p.N) = w;
+      for (int c = 0; c < kCols / 32; ++c) {
+        if (32 * c >= cols) break;
+#pragma unroll
+        for (int j = 32 * c; j < 32 * c + 32; j += 2) {
+          const uint32_t own = pack_out<kFp16>(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+          const uint32_t got = __shfl_xor_sync(0xffffffffu, own, 1);
+          if (j < left) *reinterpret_cast<uint32_t*>(dst) = __byte_perm(own, got, pick);
+          dst += step;
+        }
       }
     }
   }
@@ -434,7 +453,7 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-template <int kTok>
+template <int kTok, bool kFp16>
 cudaError_t launch(const Params& p, const uint8_t* codes, cudaStream_t st) {
   const EncodeTiledFn enc = encode_fn();
   if (enc == nullptr) return cudaErrorNotSupported;
@@ -450,18 +469,41 @@ cudaError_t launch(const Params& p, const uint8_t* codes, cudaStream_t st) {
     return cudaErrorInvalidValue;
   const size_t smem = sizeof(Smem<kTok>) + 1024;
   static_assert(sizeof(Smem<kTok>) + 1024 <= 232448, "shared memory of a CTA");
-  auto kern = mxfp4_gemm_kernel<kTok>;
+  auto kern = mxfp4_gemm_kernel<kTok, kFp16>;
   const cudaError_t e =
       ensure_max_dynamic_smem(reinterpret_cast<const void*>(kern), static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   // No more CTAs than tiles there can be.
-  const long long most = (p.R / kTok + std::min(p.E, p.R)) * static_cast<long long>(p.nb_n);
+  const long long most = (p.R / p.cap + std::min(p.E, p.R)) * static_cast<long long>(p.nb_n);
   const int grid = static_cast<int>(std::min<long long>(sm_count(), most));
   return launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, map, p);
 }
 
 // Small token tiles (twice the stages) while the average group fits one.
 bool small_tiles(int R, int E) { return R <= 64ll * E; }
+
+// Most tokens of a tile of the large variant.  A K block of a tile of n tokens
+// costs about kBlockClocks + kTokenClocks * n clocks, and a launch as many tiles
+// one after another as there are waves; group sizes are known on the device
+// only, so the groups are taken as equal.
+constexpr double kBlockClocks = 300, kTokenClocks = 1.75;
+int tile_cap(int R, int E, int nb_n) {
+  const long long groups = std::min(E, R), rows = (R + groups - 1) / groups;
+  const int ctas = sm_count();
+  int best = 256;
+  double least = 0;
+  for (int cap = 256; cap >= 64; cap -= 16) {
+    const long long per = (rows + cap - 1) / cap, tiles = per * groups * nb_n;
+    const long long size = ((rows + per - 1) / per + 15) / 16 * 16;
+    const double cost =
+        static_cast<double>((tiles + ctas - 1) / ctas) * (kBlockClocks + kTokenClocks * size);
+    if (cap == 256 || cost < least) {
+      least = cost;
+      best = cap;
+    }
+  }
+  return best;
+}
 
 bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
@@ -473,7 +515,7 @@ extern "C" {
 moe_status moe_mxfp4_clear_error(void* workspace, moe_stream_t stream) {
   if (workspace == nullptr) return MOE_ERR_INVALID_ARG;
   if (!moe::aligned_to(workspace, 256)) return MOE_ERR_ALIGNMENT;
-  return cudaMemsetAsync(workspace, 0, 4, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+  return cudaMemsetAsync(workspace, 0, 256, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? MOE_OK
              : MOE_ERR_CUDA;
 }
@@ -524,11 +566,15 @@ moe_status moe_mxfp4_gemm(const uint8_t* codes, const uint8_t* scales, const int
   p.w_sf = w_scales_chunked;
   p.scales = scales;
   p.out = static_cast<uint16_t*>(out);
-  p.fp16 = dtype == MOE_T_FP16;
   p.err = static_cast<uint32_t*>(workspace);
+  const bool small = moe::small_tiles(R, E);
+  p.cap = small ? 64 : moe::tile_cap(R, E, p.nb_n);
   auto st = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = moe::small_tiles(R, E) ? moe::launch<64>(p, codes, st)
-                                               : moe::launch<256>(p, codes, st);
+  const bool fp16 = dtype == MOE_T_FP16;
+  const cudaError_t e = small ? (fp16 ? moe::launch<64, true>(p, codes, st)
+                                      : moe::launch<64, false>(p, codes, st))
+                              : (fp16 ? moe::launch<256, true>(p, codes, st)
+                                      : moe::launch<256, false>(p, codes, st));
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
