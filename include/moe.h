@@ -329,7 +329,8 @@ moe_status moe_unpermute_backward(const void *dout, const void *rows, int dtype,
                                   float *dw, moe_stream_t stream);
 
 /* ---- MXFP4: E2M1 codes with one UE8M0 scale per 32 elements of a row. -------
- * Codes are u8 [R, K/2], element 2i in the low nibble of byte i; K % 32 == 0.
+ * Codes are u8 [R, K/2], element 2i in the low nibble of byte i; K % 32 == 0,
+ * K <= 2^30.
  * Scale bytes come in one of two layouts:
  *   MOE_SCALES_ROW_MAJOR    u8 [R, K/32], the layout of the layer's MXFP4 weights
  *   MOE_SCALES_GROUP_MAJOR  u8 [ceil(K/128), R, 4]: byte (g, r, j) scales row r's
@@ -345,7 +346,7 @@ typedef enum { MOE_SCALES_ROW_MAJOR = 0, MOE_SCALES_GROUP_MAJOR = 1 } moe_scale_
  * With inv (as for the row operators) the T tokens' rows are written once per
  * routed slot, straight into expert order: codes and scales have R = T*k rows,
  * and rows that no slot names are left as they were.  inv NULL (then k must be
- * 1): R = T, in order.  x and codes 16-byte, scales 4-byte aligned.
+ * 1): R = T, in order.  x 32-byte, codes 16-byte, scales 4-byte aligned.
  * Source: the MXFP4 weights of the FP8/FP4 variant (fw-ai/DeepGEMM PR #16,
  * Overview); the pages show no quantiser for them.
  */
@@ -355,7 +356,7 @@ moe_status moe_quantize_mxfp4(const void *x, int dtype, int T, int K, int k, con
 
 /* out[r, c] = E2M1 code * 2^(scale byte - 127), out [R, K] of `dtype`: exact in
  * bf16 and fp32 below 2^128 and infinity from there on (fp16 rounds to nearest,
- * to infinity past its range); NaN for scale byte 255.
+ * to infinity past its range); NaN for scale byte 255.  out 32-byte aligned.
  * No counterpart on the pages.
  */
 moe_status moe_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, int scale_layout,

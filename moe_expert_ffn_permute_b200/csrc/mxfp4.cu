@@ -24,6 +24,7 @@ constexpr int kThreads = 256;
 constexpr int kSlotGroup = 8;    // slots whose stores are issued together
 constexpr int kUnit = 16;        // elements a thread owns: half a block
 constexpr int kGroupUnits = 8;   // threads of a 128-wide group (four blocks)
+constexpr int kMaxRow = 1 << 30; // elements of a row (K rounded up still fits an int)
 
 // UE8M0 byte of a block from the largest magnitude's fp32 bits: 6 = 1.5 * 2^2,
 // so with amax = m * 2^e, m in [1, 2), n = e - 2 if m <= 1.5, else e - 1.
@@ -34,15 +35,51 @@ __device__ __forceinline__ int mx_scale_byte(uint32_t amax_bits) {
   return byte < 0 ? 0 : byte;
 }
 
-// Two fp32 -> two E2M1 codes, round to nearest even; `lo` in the low nibble.
-__device__ __forceinline__ uint32_t cvt_e2m1x2(float lo, float hi) {
+// Eight fp32 -> eight E2M1 codes, round to nearest even, the first in the lowest
+// nibble.
+__device__ __forceinline__ uint32_t cvt_e2m1x8(const float (&f)[8]) {
   uint32_t r;
-  asm("{\n\t.reg .b8 b;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\t"
-      "cvt.u32.u8 %0, b;\n\t}"
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
       : "=r"(r)
-      : "f"(hi), "f"(lo));
+      : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
   return r;
+}
+
+// 32 bytes in one instruction: a thread's 16-bit unit, or half of its fp32 one.
+struct alignas(32) Vec32 {
+  uint32_t w[8];
+};
+__device__ __forceinline__ Vec32 load32_stream(const Vec32* p) {
+  Vec32 v;
+  asm volatile("ld.global.cs.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]), "=r"(v.w[4]),
+                 "=r"(v.w[5]), "=r"(v.w[6]), "=r"(v.w[7])
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ void store32(Vec32* p, const Vec32& v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v.w[0]),
+               "r"(v.w[1]), "r"(v.w[2]), "r"(v.w[3]), "r"(v.w[4]), "r"(v.w[5]), "r"(v.w[6]),
+               "r"(v.w[7])
+               : "memory");
+}
+
+// i / d and i % d; in 32 bits where i fits them (a 64-bit division costs more
+// than the rest of an index).
+__device__ __forceinline__ long long divide(long long i, int d, int& rest) {
+  if (i >> 32 == 0) {
+    const uint32_t q = static_cast<uint32_t>(i) / static_cast<uint32_t>(d);
+    rest = static_cast<int>(static_cast<uint32_t>(i) - q * d);
+    return q;
+  }
+  const long long q = i / d;
+  rest = static_cast<int>(i - q * d);
+  return q;
 }
 
 // Address of the scale byte of row r, 32-wide block b, in one of the layouts.
@@ -51,79 +88,103 @@ __device__ __forceinline__ long long scale_at(long long r, int b, long long R, i
   return kGroupMajor ? ((b >> 2) * R + r) * 4 + (b & 3) : r * blocks + b;
 }
 
+// What a thread reads of a unit, its largest magnitude (as fp32 bits: compared
+// as integers, infinities and NaN rank above all others; 16-bit types two at a
+// time) and its elements in fp32.
+template <int kDtype>
+struct Unit {
+  static constexpr int kVecs = kDtype == MOE_T_FP32 ? 2 : 1;
+  Vec32 v[kVecs];
+
+  __device__ __forceinline__ uint32_t amax_bits() const {
+    uint32_t top = 0;
+    if constexpr (kDtype == MOE_T_FP32) {
+#pragma unroll
+      for (int c = 0; c < 16; ++c) top = max(top, v[c >> 3].w[c & 7] & 0x7FFFFFFFu);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) top = __vmaxu2(top, v[0].w[c] & 0x7FFF7FFFu);
+      top = max(top >> 16, top & 0xFFFFu);
+      if constexpr (kDtype == MOE_T_BF16)
+        top <<= 16;
+      else
+        top = __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(top))));
+    }
+    return top;
+  }
+  // Elements 8h .. 8h + 7.
+  __device__ __forceinline__ void get(int h, float (&f)[8]) const {
+    if constexpr (kDtype == MOE_T_FP32) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) f[c] = __uint_as_float(v[h].w[c]);
+    } else {
+      Elem<kDtype>::unpack(
+          make_uint4(v[0].w[4 * h], v[0].w[4 * h + 1], v[0].w[4 * h + 2], v[0].w[4 * h + 3]), f);
+    }
+  }
+};
+
 // One thread per 16 elements; eight consecutive threads share a 128-wide group
-// of a row and write its four scale bytes as one word.  The threads of a row
-// are rounded up to whole groups, so a group never straddles two rows.
+// of a row and write its four scale bytes as one word.  The threads of a row are
+// rounded up to whole groups, so a group never straddles two rows.
 template <int kDtype, bool kGroupMajor>
 __global__ void __launch_bounds__(kThreads) quantize_mxfp4_kernel(
-    const uint4* __restrict__ x, const int32_t* __restrict__ inv, int T, int K, int k,
+    const Vec32* __restrict__ x, const int32_t* __restrict__ inv, int T, int K, int k,
     uint2* __restrict__ codes, uint8_t* __restrict__ scales) {
-  using E = Elem<kDtype>;
-  constexpr int kVecs = kUnit / E::kPerVec;
   griddep_launch_dependents();
   griddep_wait();
-  const int groups = (K + 127) / 128;
-  const int units = K / kUnit;
+  const int units = K / kUnit, blocks = K / 32;
+  const long long R = static_cast<long long>(T) * k;
   const long long i = blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x;
-  const long long gid = i / kGroupUnits;
-  const long long t = gid / groups;
-  const int g = static_cast<int>(gid - t * groups);
-  const int u = g * kGroupUnits + static_cast<int>(i % kGroupUnits);
+  const int lane8 = threadIdx.x % kGroupUnits;
+  int g;
+  const long long t = divide(i / kGroupUnits, (K + 127) / 128, g);
+  const int u = g * kGroupUnits + lane8;
   const bool live = t < T && u < units;
-  uint4 v[kVecs];
+  Unit<kDtype> unit;
 #pragma unroll
-  for (int q = 0; q < kVecs; ++q)
-    v[q] = live ? __ldcs(x + (t * units + u) * kVecs + q) : make_uint4(0, 0, 0, 0);
-  float f[kUnit];
-#pragma unroll
-  for (int q = 0; q < kVecs; ++q) {
-    float part[E::kPerVec];
-    E::unpack(v[q], part);
-#pragma unroll
-    for (int c = 0; c < E::kPerVec; ++c) f[q * E::kPerVec + c] = part[c];
-  }
-  // Magnitudes compared as integers: infinities and NaN rank above all others.
-  uint32_t amax = 0;
-#pragma unroll
-  for (int c = 0; c < kUnit; ++c) amax = max(amax, __float_as_uint(f[c]) & 0x7FFFFFFFu);
+  for (int q = 0; q < Unit<kDtype>::kVecs; ++q)
+    unit.v[q] = live ? load32_stream(x + (t * units + u) * Unit<kDtype>::kVecs + q) : Vec32{};
+  uint32_t amax = unit.amax_bits();
   amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
   const int byte = mx_scale_byte(amax);
   const float inv_scale = __uint_as_float(static_cast<uint32_t>(254 - byte) << 23);   // 2^-n
-  uint2 out = make_uint2(0, 0);
+  uint32_t out[2] = {0, 0};
   if (byte != 255) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      out.x |= cvt_e2m1x2(f[2 * c] * inv_scale, f[2 * c + 1] * inv_scale) << (8 * c);
-      out.y |= cvt_e2m1x2(f[8 + 2 * c] * inv_scale, f[8 + 2 * c + 1] * inv_scale) << (8 * c);
+    for (int h = 0; h < 2; ++h) {
+      float f[8];
+      unit.get(h, f);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) f[c] *= inv_scale;
+      out[h] = cvt_e2m1x8(f);
     }
   }
-  // The group's four bytes (0 for blocks past K) on its first thread.
-  uint32_t word = live ? static_cast<uint32_t>(byte) << (8 * ((threadIdx.x >> 1) & 3)) : 0u;
+  // The group's four bytes (0 for blocks past K).
+  uint32_t word = live ? static_cast<uint32_t>(byte) << (8 * (lane8 >> 1)) : 0u;
   word |= __shfl_xor_sync(0xffffffffu, word, 2);
   word |= __shfl_xor_sync(0xffffffffu, word, 4);
   if (t >= T) return;
-  const long long R = static_cast<long long>(T) * k;
-  const int blocks = K / 32;
+  auto write = [&](long long r) {
+    if (r < 0 || r >= R) return;
+    if (live) codes[r * units + u] = make_uint2(out[0], out[1]);
+    if (kGroupMajor || blocks % 4 == 0) {
+      if (lane8 == 0)
+        *reinterpret_cast<uint32_t*>(scales + scale_at<kGroupMajor>(r, 4 * g, R, blocks)) = word;
+    } else if (live && (lane8 & 1) == 0) {
+      scales[scale_at<false>(r, u >> 1, R, blocks)] = static_cast<uint8_t>(byte);
+    }
+  };
+  if (inv == nullptr) {
+    write(t);
+    return;
+  }
   for (int j0 = 0; j0 < k; j0 += kSlotGroup) {
     int p[kSlotGroup];
 #pragma unroll
-    for (int j = 0; j < kSlotGroup; ++j)
-      p[j] = j0 + j >= k ? -1 : (inv != nullptr ? __ldg(&inv[t * k + j0 + j]) : static_cast<int>(t));
+    for (int j = 0; j < kSlotGroup; ++j) p[j] = j0 + j < k ? __ldg(&inv[t * k + j0 + j]) : -1;
 #pragma unroll
-    for (int j = 0; j < kSlotGroup; ++j) {
-      const long long r = p[j];
-      if (r < 0 || r >= R) continue;
-      if (live) codes[r * units + u] = out;
-      if (kGroupMajor) {
-        if ((threadIdx.x & 7) == 0)
-          *reinterpret_cast<uint32_t*>(scales + scale_at<true>(r, 4 * g, R, blocks)) = word;
-      } else if (blocks % 4 == 0) {
-        if ((threadIdx.x & 7) == 0)
-          *reinterpret_cast<uint32_t*>(scales + scale_at<false>(r, 4 * g, R, blocks)) = word;
-      } else if (live && (threadIdx.x & 1) == 0) {
-        scales[scale_at<false>(r, u >> 1, R, blocks)] = static_cast<uint8_t>(byte);
-      }
-    }
+    for (int j = 0; j < kSlotGroup; ++j) write(p[j]);
   }
 }
 
@@ -131,16 +192,16 @@ __global__ void __launch_bounds__(kThreads) quantize_mxfp4_kernel(
 template <int kDtype, bool kGroupMajor>
 __global__ void __launch_bounds__(kThreads) dequantize_mxfp4_kernel(
     const uint2* __restrict__ codes, const uint8_t* __restrict__ scales, long long R, int K,
-    uint4* __restrict__ out) {
+    Vec32* __restrict__ out) {
   using E = Elem<kDtype>;
-  constexpr int kVecs = kUnit / E::kPerVec;
+  constexpr int kPer = 32 / E::kBytes;   // values of a 32-byte store
   griddep_launch_dependents();
   griddep_wait();
   const int units = K / kUnit;
   const long long i = blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x;
   if (i >= R * units) return;
-  const long long r = i / units;
-  const int u = static_cast<int>(i - r * units);
+  int u;
+  const long long r = divide(i, units, u);
   const uint2 v = __ldcs(codes + i);
   const int byte = __ldg(scales + scale_at<kGroupMajor>(r, u >> 1, R, K / 32));
   // 2^(byte - 127): byte 0 is a subnormal, byte 255 NaN.
@@ -149,18 +210,27 @@ __global__ void __launch_bounds__(kThreads) dequantize_mxfp4_kernel(
                                                               : static_cast<uint32_t>(byte) << 23);
   const uint32_t w[2] = {v.x, v.y};
 #pragma unroll
-  for (int q = 0; q < kVecs; ++q) {
-    float f[E::kPerVec];
+  for (int q = 0; q < kUnit / kPer; ++q) {
+    Vec32 o;
 #pragma unroll
-    for (int c = 0; c < E::kPerVec; ++c) {
-      const int at = q * E::kPerVec + c;
-      const uint32_t code = (w[at >> 3] >> (4 * (at & 7))) & 15u;
-      // Exponent and mantissa bits read as an fp32 of exponent bias 127: times
-      // 2^126 they have E2M1's bias 1, its subnormal 0.5 included.
-      const float mag = __uint_as_float((code & 7u) << 22) * 8.507059173023462e37f;
-      f[c] = __uint_as_float(__float_as_uint(mag) | (code & 8u) << 28) * scale;
+    for (int h = 0; h < 2; ++h) {
+      float f[E::kPerVec];
+#pragma unroll
+      for (int c = 0; c < E::kPerVec; ++c) {
+        const int at = q * kPer + h * E::kPerVec + c;
+        const uint32_t code = (w[at >> 3] >> (4 * (at & 7))) & 15u;
+        // Exponent and mantissa bits read as an fp32 of exponent bias 127: times
+        // 2^126 they have E2M1's bias 1, its subnormal 0.5 included.
+        const float mag = __uint_as_float((code & 7u) << 22) * 8.507059173023462e37f;
+        f[c] = __uint_as_float(__float_as_uint(mag) | (code & 8u) << 28) * scale;
+      }
+      const uint4 half = E::pack(f);
+      o.w[4 * h] = half.x;
+      o.w[4 * h + 1] = half.y;
+      o.w[4 * h + 2] = half.z;
+      o.w[4 * h + 3] = half.w;
     }
-    out[i * kVecs + q] = E::pack(f);
+    store32(out + i * (kUnit / kPer) + q, o);
   }
 }
 
@@ -247,7 +317,7 @@ cudaError_t launch_quantize(bool group_major, unsigned blocks, cudaStream_t st, 
                             uint8_t* scales) {
   auto kern = group_major ? quantize_mxfp4_kernel<kDtype, true>
                           : quantize_mxfp4_kernel<kDtype, false>;
-  return launch_pdl(kern, dim3(blocks), dim3(kThreads), 0, st, static_cast<const uint4*>(x), inv,
+  return launch_pdl(kern, dim3(blocks), dim3(kThreads), 0, st, static_cast<const Vec32*>(x), inv,
                     T, K, k, reinterpret_cast<uint2*>(codes), scales);
 }
 
@@ -259,7 +329,7 @@ cudaError_t launch_dequantize(bool group_major, unsigned blocks, cudaStream_t st
                           : dequantize_mxfp4_kernel<kDtype, false>;
   return launch_pdl(kern, dim3(blocks), dim3(kThreads), 0, st,
                     reinterpret_cast<const uint2*>(codes), scales, static_cast<long long>(R), K,
-                    static_cast<uint4*>(out));
+                    static_cast<Vec32*>(out));
 }
 
 // Tiles of prepacked weights, or 0 for sizes the product does not take.
@@ -281,8 +351,8 @@ moe_status moe_quantize_mxfp4(const void* x, int dtype, int T, int K, int k, con
   if (T < 1 || K < 1 || k < 1 || static_cast<long long>(T) * k >= (1ll << 31))
     return MOE_ERR_INVALID_ARG;
   if (inv == nullptr && k != 1) return MOE_ERR_INVALID_ARG;
-  if (K % 32 != 0) return MOE_ERR_UNSUPPORTED;
-  if (!moe::aligned_to(x, 16) || !moe::aligned_to(codes, 16) || !moe::aligned_to(scales, 4) ||
+  if (K % 32 != 0 || K > moe::kMaxRow) return MOE_ERR_UNSUPPORTED;
+  if (!moe::aligned_to(x, 32) || !moe::aligned_to(codes, 16) || !moe::aligned_to(scales, 4) ||
       !moe::aligned_to(inv, 4))
     return MOE_ERR_ALIGNMENT;
   const long long R = static_cast<long long>(T) * k;
@@ -307,8 +377,8 @@ moe_status moe_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, int
   if (codes == nullptr || scales == nullptr || out == nullptr) return MOE_ERR_INVALID_ARG;
   if (!moe::elem_ok(dtype) || !moe::layout_ok(scale_layout) || R < 1 || K < 1)
     return MOE_ERR_INVALID_ARG;
-  if (K % 32 != 0) return MOE_ERR_UNSUPPORTED;
-  if (!moe::aligned_to(codes, 16) || !moe::aligned_to(out, 16)) return MOE_ERR_ALIGNMENT;
+  if (K % 32 != 0 || K > moe::kMaxRow) return MOE_ERR_UNSUPPORTED;
+  if (!moe::aligned_to(codes, 16) || !moe::aligned_to(out, 32)) return MOE_ERR_ALIGNMENT;
   const long long n = R * static_cast<long long>(K);
   if (moe::buffers_overlap(codes, n / 2, out, n * moe::elem_bytes(dtype)) ||
       moe::buffers_overlap(scales, moe::scale_bytes(R, K, scale_layout), out,

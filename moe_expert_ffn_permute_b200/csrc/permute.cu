@@ -13,6 +13,8 @@
 // once and writes each output row once.
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "elem.cuh"
 #include "internal.h"
 #include "sm100.cuh"
@@ -55,8 +57,8 @@ __global__ void __launch_bounds__(kThreads) permute_kernel(const V* __restrict__
     for (int j = 0; j < kSlotGroup; ++j) {
       if (!routed(p[j], S)) continue;
       V* row = rows + p[j] * vecs;
-      row[c] = v0;
-      if (second) row[c + half] = v1;
+      __stcs(row + c, v0);
+      if (second) __stcs(row + c + half, v1);
     }
   }
 }
@@ -112,7 +114,7 @@ __global__ void __launch_bounds__(kThreads) unpermute_kernel(
       }
     }
   }
-  out[t * vecs + c] = E::pack(acc[0]);
+  __stcs(out + t * vecs + c, E::pack(acc[0]));
   if (second) out[t * vecs + c + half] = E::pack(acc[1]);
 }
 
@@ -165,7 +167,7 @@ __global__ void __launch_bounds__(kThreads) unpermute_backward_kernel(
         float g[E::kPerVec];
 #pragma unroll
         for (int q = 0; q < E::kPerVec; ++q) g[q] = w[j] * d[q];
-        drows[p[j] + c] = E::pack(g);
+        __stcs(drows + p[j] + c, E::pack(g));
       }
     }
   }
@@ -232,8 +234,13 @@ template <int kDtype, int kJ>
 cudaError_t launch_backward(const void* dout, const void* rows, const int32_t* inv,
                             const float* topk_w, int T, long long vecs, int k, void* drows,
                             float* dw, cudaStream_t st) {
-  // As few threads as give each the same number of chunks.
-  const long long rounds = (vecs + kThreads - 1) / kThreads;
+  // Threads that each take the same number of chunks of the row: as many as
+  // there may be where a block has one slot; with four, blocks of about seven
+  // chunks a thread (128 threads on rows of 14 KB: 150 us against 155 with 224;
+  // 256 on rows of 28 KB: 84 us against 88 with 128).
+  const long long fewest = (vecs + kThreads - 1) / kThreads;
+  const long long rounds =
+      kJ == 1 ? fewest : std::max(fewest, std::min(7ll, (vecs + 127) / 128));
   const unsigned threads = static_cast<unsigned>(((vecs + rounds - 1) / rounds + 31) / 32 * 32);
   const unsigned blocks = static_cast<unsigned>(T) * ((k + kJ - 1) / kJ);
   return launch_pdl(unpermute_backward_kernel<kDtype, kJ>, dim3(blocks), dim3(threads), 0, st,
@@ -241,8 +248,11 @@ cudaError_t launch_backward(const void* dout, const void* rows, const int32_t* i
                     T, vecs, k, static_cast<uint4*>(drows), dw);
 }
 
-// Below this many tokens a block takes one slot instead of up to eight: a
-// token's slots then spread over the SMs.
+// Slots of a token that a block of the gradient takes: four (4096 tokens, top-8,
+// 7168 wide in bf16: 155 us; eight take 163 us, their 109 registers leave few
+// blocks per SM; two 171, one 173, re-reading dout), or one below this many
+// tokens, where a token's slots should spread over the SMs.
+constexpr int kBackSlots = 4;
 constexpr int kSlotBlocksBelow = 2 * 148;
 
 template <int kDtype>
@@ -251,7 +261,7 @@ cudaError_t launch_backward_any(const void* dout, const void* rows, const int32_
                                 float* dw, cudaStream_t st) {
   if (T < kSlotBlocksBelow || k == 1)
     return launch_backward<kDtype, 1>(dout, rows, inv, topk_w, T, vecs, k, drows, dw, st);
-  return launch_backward<kDtype, kSlotGroup>(dout, rows, inv, topk_w, T, vecs, k, drows, dw, st);
+  return launch_backward<kDtype, kBackSlots>(dout, rows, inv, topk_w, T, vecs, k, drows, dw, st);
 }
 
 }  // namespace

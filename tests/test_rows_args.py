@@ -73,6 +73,10 @@ CASES = [
     ("moe_quantize_mxfp4", UNSUPPORTED, dict(K=48)),
     ("moe_quantize_mxfp4", ALIGNMENT, dict(scales=D + 2)),
     ("moe_quantize_mxfp4", ALIGNMENT, dict(codes=C + 8)),
+    ("moe_quantize_mxfp4", ALIGNMENT, dict(x=A + 16)),
+    ("moe_quantize_mxfp4", UNSUPPORTED, dict(T=1, k=1, inv=None, K=(1 << 30) + 32)),
+    ("moe_dequantize_mxfp4", ALIGNMENT, dict(out=C + 16)),
+    ("moe_dequantize_mxfp4", UNSUPPORTED, dict(R=1, K=(1 << 30) + 32)),
     ("moe_dequantize_mxfp4", INVALID, dict(R=0)), ("moe_dequantize_mxfp4", INVALID, dict(out=A)),
     ("moe_dequantize_mxfp4", INVALID, dict(out=B)), ("moe_dequantize_mxfp4", INVALID, dict(scales=None)),
     ("moe_dequantize_mxfp4", UNSUPPORTED, dict(K=16)),
