@@ -579,13 +579,17 @@ def moe_mxfp4_gemm(codes, scales, offsets, R, E, N, K, w_tiled, w_scales_chunked
     _sizes(fn, R, E, N, K)
     z, at = _ELEM[dtype], _device()
     tiles = _weight_tiles(E, N, K)
+    # (Only products on CTA pairs need more than the error word's 256 bytes, and
+    # they have at least 224 rows per group: small calls skip the question.)
+    need = 256 if R < 224 * E else lib().moe_mxfp4_workspace_bytes(R, E, N, K)
     _check(lib().moe_mxfp4_gemm(
         _buf(fn, "codes", codes, R * (K // 2), "u8", at),
         _buf(fn, "scales", scales, _scale_bytes(R, K, 1), "u8", at),
         _buf(fn, "offsets", offsets, 4 * (E + 1), "i32", at), R, E, N, K,
         _buf(fn, "w_tiled", w_tiled, tiles * 16384, "u8", at),
         _buf(fn, "w_scales_chunked", w_scales_chunked, tiles * 1024, "u8", at), d,
-        _buf(fn, "out", out, R * N * z, dtype, at), _buf(fn, "workspace", workspace, 256, "any", at),
+        _buf(fn, "out", out, R * N * z, dtype, at), 
+        _buf(fn, "workspace", workspace, need, "any", at),
         _stream(stream)), fn)
 
 

@@ -31,19 +31,26 @@
 
 #include "elem.cuh"
 #include "internal.h"
+#include "mxfp4_tiles.cuh"
 #include "sm100.cuh"
 
 namespace moe {
 namespace {
 
+using mx::kKBytes;
+using mx::Tile;
+using mx::tile_at;
+using mx::uniform;
+
 constexpr int kThreads = 384;
 constexpr int kEpiWarps = 8;
 constexpr uint32_t kTmemCols = 512;
-constexpr int kKBytes = 128;             // bytes of a row per stage: 256 codes
 // TMEM: the accumulator takes columns 0..255; two scale sets, used in turn so
 // that a copy never lands in the set that MMAs just issued may still read.  A
 // set holds 2 x 4 columns of weight scales and 2 x 8 of token scales (rows
-// 0..127 and 128..255 of the tile, for each half of the stage's K).
+// 0..127 and 128..255 of the tile, for each half of the stage's K).  (Two
+// accumulators of 224 columns used in turn measured the same at equal tiles, and
+// the smaller tiles cost 10%: the epilogue frees TMEM as soon as it has loaded.)
 constexpr uint32_t kSfCol = 256, kSfSet = 32, kSfTokens = 8;
 
 // kTok: most tokens of a tile.  256: the fewest weight reads per token; 64: twice
@@ -66,82 +73,18 @@ struct __align__(1024) Smem {
   uint64_t full_sf[C::kStages];   // the scale warps' copies
   uint64_t empty[C::kStages];
   uint64_t tmem_full, tmem_empty, drain;
-  int row_off[kMxMaxExperts + 1];    // first row of each expert, made monotone
-  int tile_off[kMxMaxExperts + 1];   // token tiles before each expert
+  mx::Groups groups;
   uint32_t tmem_base;
   int abort_flag;
 };
-
-struct Params {
-  int R, E, N, K;
-  int cap;                    // most tokens of a tile (a multiple of 16, at most kTok)
-  int nb_n, kb_n;             // 128-row weight blocks, 256-wide K blocks
-  const int32_t* offsets;     // null: one group of all rows
-  const uint8_t* w;           // prepacked tiles
-  const uint8_t* w_sf;        // prepacked scale chunks
-  const uint8_t* scales;      // token scales, group-major [ceil(K/128)][R][4]
-  uint16_t* out;
-  uint32_t* err;
-};
-
-struct Tile {
-  int e, nb, row, rows;       // expert, weight block, first row, rows (1..cap)
-};
-
-// Tile `id` of the launch: the groups' token tiles in order, each with all its
-// weight blocks.  A group is cut into tiles of equal size (a multiple of 16).
-template <int kTok>
-__device__ __forceinline__ Tile tile_at(const Smem<kTok>& sm, const Params& p, long long id) {
-  Tile t;
-  const int tt = static_cast<int>(id / p.nb_n);
-  t.nb = static_cast<int>(id - static_cast<long long>(tt) * p.nb_n);
-  int lo = 0, hi = p.E - 1;   // the last expert whose tiles start at or before tt
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (sm.tile_off[mid] <= tt) lo = mid;
-    else hi = mid - 1;
-  }
-  // Experts without rows share their successor's start: the search lands on the
-  // last of equals, which is the one that has the tile.
-  t.e = lo;
-  const int n = sm.row_off[lo + 1] - sm.row_off[lo];
-  const int tiles = sm.tile_off[lo + 1] - sm.tile_off[lo];
-  const int size = ((n + tiles - 1) / tiles + 15) & ~15;
-  const int local = (tt - sm.tile_off[lo]) * size;
-  t.row = sm.row_off[lo] + local;
-  t.rows = min(size, n - local);
-  return t;
-}
-
-// The value on lane 0: the same on every lane, and the compiler knows it.
-template <class T>
-__device__ __forceinline__ T uniform(T v) {
-  return __shfl_sync(0xffffffffu, v, 0);
-}
 
 __device__ __forceinline__ uint32_t mma_n(int rows) {
   return static_cast<uint32_t>((rows + 15) & ~15);
 }
 
-// Two fp32 -> two 16-bit floats, round to nearest even; `lo` in the low half.
-template <bool kFp16>
-__device__ __forceinline__ uint32_t pack_out(float lo, float hi) {
-  if constexpr (kFp16) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-  } else {
-    return pack_bf16x2(lo, hi);
-  }
-}
-
-// Token columns [c0, c0 + cols) of an accumulator of n columns are half h's: the
-// two warps of a sub-partition share a tile's tokens evenly.
-__device__ __forceinline__ int half_begin(int n, int h) { return h ? (n / 2 + 7) & ~7 : 0; }
-
 template <int kTok, bool kFp16>
 __global__ void __launch_bounds__(kThreads, 1)
-    mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap, const Params p) {
+    mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap, const MxGemm p) {
   using C = Cfg<kTok>;
   constexpr int STAGES = C::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -171,53 +114,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // Everything above is local set-up that overlaps the previous kernel's tail.
   griddep_wait();
-  if (warp == 2) {
-    // Row offsets, clamped to [0, R] and made monotone (a running maximum), so
-    // that no content of the array can lead outside the buffers; then the
-    // prefix sums of the token tiles.
-    if (p.offsets == nullptr) {
-      if (lane == 0) {
-        sm.row_off[0] = 0;
-        sm.row_off[1] = p.R;
-      }
-    } else {
-      int carry = 0;
-      for (int b = 0; b <= p.E; b += 32) {
-        const int i = b + lane;
-        int v = i <= p.E ? min(max(__ldg(&p.offsets[i]), 0), p.R) : 0;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int u = __shfl_up_sync(0xffffffffu, v, o);
-          if (lane >= o) v = max(v, u);
-        }
-        v = max(v, carry);
-        carry = __shfl_sync(0xffffffffu, v, 31);
-        if (i <= p.E) sm.row_off[i] = v;
-      }
-    }
-    __syncwarp();
-    int carry = 0;
-    for (int b = 0; b < p.E; b += 32) {
-      const int i = b + lane;
-      const int rows = i < p.E ? sm.row_off[i + 1] - sm.row_off[i] : 0;
-      const int own = (rows + p.cap - 1) / p.cap;
-      int v = own;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += u;
-      }
-      if (i < p.E) sm.tile_off[i] = carry + v - own;
-      carry += __shfl_sync(0xffffffffu, v, 31);
-    }
-    if (lane == 0) sm.tile_off[p.E] = carry;
-  }
+  if (warp == 2) mx::find_groups(sm.groups, p.offsets, p.R, p.E, p.cap);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
   const int kb_n = p.kb_n;
-  const long long tiles = static_cast<long long>(sm.tile_off[p.E]) * p.nb_n;
+  const long long tiles = static_cast<long long>(sm.groups.tile_off[p.E]) * p.nb_n;
   const int my_tiles = uniform(
       static_cast<int>((tiles - blockIdx.x + gridDim.x - 1) / gridDim.x));   // may be <= 0
 
@@ -233,9 +136,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     long long issued = 0;   // stages filled
     bool ok = true;
     for (int i = 0; ok && i < my_tiles; ++i) {
-      const Tile t = tile_at<kTok>(sm, p, blockIdx.x + static_cast<long long>(i) * gridDim.x);
+      const Tile t =
+          tile_at(sm.groups, p.E, p.nb_n, blockIdx.x + static_cast<long long>(i) * gridDim.x);
       // Weights of an expert with one token tile are read once.
-      const uint64_t pol_w = sm.tile_off[t.e + 1] - sm.tile_off[t.e] > 1 ? pol_reused : pol_once;
+      const uint64_t pol_w =
+          sm.groups.tile_off[t.e + 1] - sm.groups.tile_off[t.e] > 1 ? pol_reused : pol_once;
       const int boxes = uniform((t.rows + C::kBox - 1) / C::kBox);
       const uint32_t bytes = kTileBytes + 1024 + boxes * C::kBox * kKBytes;
       const long long block = uniform((static_cast<long long>(t.e) * p.nb_n + t.nb) * kb_n);
@@ -280,7 +185,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t phase = 0;
     bool ok = true;
     for (int i = 0; ok && i < my_tiles; ++i) {
-      const Tile t = tile_at<kTok>(sm, p, blockIdx.x + static_cast<long long>(i) * gridDim.x);
+      const Tile t =
+          tile_at(sm.groups, p.E, p.nb_n, blockIdx.x + static_cast<long long>(i) * gridDim.x);
       const int quads = (t.rows + 31) / 32;
       for (int kb = 0; kb < kb_n; ++kb) {
         if (!mbar_wait(&sm.empty[stage], phase ^ 1u, p.err, &sm.abort_flag)) {
@@ -319,7 +225,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint64_t kKStep = 32 >> 4, kSfChunk = 512 >> 4;
     bool ok = true;
     for (int i = 0; ok && i < my_tiles; ++i) {
-      const Tile t = tile_at<kTok>(sm, p, blockIdx.x + static_cast<long long>(i) * gridDim.x);
+      const Tile t =
+          tile_at(sm.groups, p.E, p.nb_n, blockIdx.x + static_cast<long long>(i) * gridDim.x);
       const uint32_t n = uniform(mma_n(t.rows));
       const uint32_t idesc0 = mxf4_idesc(n, 0);
       if (!mbar_wait_warp(&sm.tmem_empty, acc_phase ^ 1u, p.err, &sm.abort_flag)) break;
@@ -384,13 +291,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int half = (warp - 4) >> 2;    // which half of the tile's token columns
     constexpr int kCols = kTok / 2;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
-    const bool odd = lane & 1;
-    const uint32_t pick = odd ? 0x3276u : 0x5410u;
     uint32_t acc_phase = 0;
     for (int i = 0; i < my_tiles; ++i) {
-      const Tile t = tile_at<kTok>(sm, p, blockIdx.x + static_cast<long long>(i) * gridDim.x);
+      const Tile t =
+          tile_at(sm.groups, p.E, p.nb_n, blockIdx.x + static_cast<long long>(i) * gridDim.x);
       const int n = static_cast<int>(mma_n(t.rows));
-      const int c0 = half_begin(n, half), cols = half ? n - c0 : half_begin(n, 1);
+      const int c0 = mx::half_begin(n, half), cols = half ? n - c0 : mx::half_begin(n, 1);
       if (!mbar_wait(&sm.tmem_full, acc_phase, p.err, &sm.abort_flag)) break;
       acc_phase ^= 1u;
       tc_fence_after();
@@ -405,25 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.tmem_empty);
-      // Lane = feature, register = token.  Neighbouring lanes trade halves of a
-      // pair of tokens so that an even lane holds two features of the first and
-      // an odd lane of the second: 4-byte stores, 64 contiguous bytes per token.
-      const int f = t.nb * 128 + q * 32 + (lane & ~1);
-      uint16_t* dst = p.out + (static_cast<size_t>(t.row) + c0 + (odd ? 1 : 0)) * p.N + f;
-      const size_t step = 2 * static_cast<size_t>(p.N);
-      // Tokens of this half, counted from the lane's first.
-      const int left = f < p.N ? min(cols, t.rows - c0) - (odd ? 1 : 0) : 0;
-#pragma unroll
-      for (int c = 0; c < kCols / 32; ++c) {
-        if (32 * c >= cols) break;
-#pragma unroll
-        for (int j = 32 * c; j < 32 * c + 32; j += 2) {
-          const uint32_t own = pack_out<kFp16>(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
-          const uint32_t got = __shfl_xor_sync(0xffffffffu, own, 1);
-          if (j < left) *reinterpret_cast<uint32_t*>(dst) = __byte_perm(own, got, pick);
-          dst += step;
-        }
-      }
+      mx::store_tile<kCols, kFp16>(v, p.out, p.N, t.nb * 128 + q * 32, t, c0, cols);
     }
   }
 
@@ -454,18 +342,9 @@ EncodeTiledFn encode_fn() {
 }
 
 template <int kTok, bool kFp16>
-cudaError_t launch(const Params& p, const uint8_t* codes, cudaStream_t st) {
-  const EncodeTiledFn enc = encode_fn();
-  if (enc == nullptr) return cudaErrorNotSupported;
+cudaError_t launch(const MxGemm& p, cudaStream_t st) {
   CUtensorMap map;
-  std::memset(&map, 0, sizeof(map));
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(p.K / 2), static_cast<cuuint64_t>(p.R)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(p.K / 2)};
-  const cuuint32_t box[2] = {kKBytes, Cfg<kTok>::kBox};
-  const cuuint32_t estr[2] = {1, 1};
-  if (enc(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(codes), dims, strides, box,
-          estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+  if (!mx::map_rows(&map, p.codes, p.K / 2, p.R, kKBytes, Cfg<kTok>::kBox, true))
     return cudaErrorInvalidValue;
   const size_t smem = sizeof(Smem<kTok>) + 1024;
   static_assert(sizeof(Smem<kTok>) + 1024 <= 232448, "shared memory of a CTA");
@@ -505,9 +384,36 @@ int tile_cap(int R, int E, int nb_n) {
   return best;
 }
 
+// CTA pairs (mxfp4_pair.cu) where the average group fills most of a 256-row tile
+// and the 256 x 256 tiles make at least four waves of pairs.  Pairs against this
+// kernel, power-capped, us: 2048 rows per group 7168 -> 4096 x 32 groups 800 / 860,
+// 2048 -> 7168 528 / 545; 256 rows per group 7168 -> 4096 x 32 154 / 162; 192 rows
+// per group 2048 -> 4096 x 64 92 / 88; one group of 4096 rows 4096 -> 4096 (3.5
+// waves) 35.5 / 35.0, of 1024 rows 7168 -> 4096 (under a wave) 17.6 / 15.4.
+bool use_pairs(int R, int E, int N) {
+  return R >= 224ll * E && (R / 256) * ((N + 255ll) / 256) >= 2ll * sm_count();
+}
+
 bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 }  // namespace
+
+bool mx::map_rows(CUtensorMap* m, const void* base, uint64_t width, uint64_t rows, uint32_t box,
+                  uint32_t box_rows, bool swizzle128) {
+  const EncodeTiledFn enc = encode_fn();
+  if (enc == nullptr) return false;
+  std::memset(m, 0, sizeof(*m));
+  const cuuint64_t dims[2] = {width, rows};
+  const cuuint64_t strides[1] = {width};
+  const cuuint32_t boxes[2] = {box, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, boxes,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace moe
 
 extern "C" {
@@ -532,7 +438,8 @@ moe_status moe_mxfp4_check_error(const void* workspace, moe_stream_t stream) {
 }
 
 size_t moe_mxfp4_workspace_bytes(int R, int E, int N, int K) {
-  return R >= 1 && moe::mx_gemm_sizes_ok(E, N, K) ? 256 : 0;
+  if (R < 1 || !moe::mx_gemm_sizes_ok(E, N, K)) return 0;
+  return 256 + (moe::use_pairs(R, E, N) ? moe::mx_pair_record_bytes(R, E, K) : 0);
 }
 
 moe_status moe_mxfp4_gemm(const uint8_t* codes, const uint8_t* scales, const int32_t* offsets,
@@ -554,7 +461,7 @@ moe_status moe_mxfp4_gemm(const uint8_t* codes, const uint8_t* scales, const int
   if (moe::buffers_overlap(out, rb * N * 2, codes, rb * (K / 2)) ||
       moe::buffers_overlap(out, rb * N * 2, scales, (K + 127) / 128 * rb * 4))
     return MOE_ERR_INVALID_ARG;
-  moe::Params p{};
+  moe::MxGemm p{};
   p.R = R;
   p.E = E;
   p.N = N;
@@ -564,17 +471,23 @@ moe_status moe_mxfp4_gemm(const uint8_t* codes, const uint8_t* scales, const int
   p.offsets = offsets;
   p.w = w_tiled;
   p.w_sf = w_scales_chunked;
+  p.codes = codes;
   p.scales = scales;
   p.out = static_cast<uint16_t*>(out);
   p.err = static_cast<uint32_t*>(workspace);
+  p.records = static_cast<uint8_t*>(workspace) + 256;
   const bool small = moe::small_tiles(R, E);
   p.cap = small ? 64 : moe::tile_cap(R, E, p.nb_n);
   auto st = reinterpret_cast<cudaStream_t>(stream);
   const bool fp16 = dtype == MOE_T_FP16;
-  const cudaError_t e = small ? (fp16 ? moe::launch<64, true>(p, codes, st)
-                                      : moe::launch<64, false>(p, codes, st))
-                              : (fp16 ? moe::launch<256, true>(p, codes, st)
-                                      : moe::launch<256, false>(p, codes, st));
+  if (moe::use_pairs(R, E, N)) {
+    p.cap = 256;
+    return moe::launch_mx_pairs(p, fp16, st) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  }
+  const cudaError_t e = small ? (fp16 ? moe::launch<64, true>(p, st)
+                                      : moe::launch<64, false>(p, st))
+                              : (fp16 ? moe::launch<256, true>(p, st)
+                                      : moe::launch<256, false>(p, st));
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 

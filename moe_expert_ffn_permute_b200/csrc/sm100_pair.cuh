@@ -128,6 +128,21 @@ __device__ __forceinline__ void mma_mxf8f6f4_pair(uint32_t d_tmem, uint64_t a_de
       : "memory");
 }
 
+// The MXFP4 x MXFP4 form (kind::mxf4, K = 64 per instruction, two scale bytes
+// per row and operand).
+__device__ __forceinline__ void mma_mxf4_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                              uint32_t idesc, uint32_t sfa_tmem,
+                                              uint32_t sfb_tmem, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], "
+      "[%6], p;\n\t"
+      "}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
+      : "memory");
+}
+
 // Arrive on the mbarrier at this shared offset in every CTA of `cta_mask`
 // once all prior tcgen05 operations of this thread have completed.
 __device__ __forceinline__ void tc_commit_pair_multicast(uint64_t* bar, uint16_t cta_mask) {
@@ -141,6 +156,13 @@ __device__ __forceinline__ void tc_commit_pair_multicast(uint64_t* bar, uint16_t
 // Instruction descriptor for M = 256 (pair) block-scaled E4M3 x E4M3.
 __host__ __device__ constexpr uint32_t mxf8f6f4_idesc_m256(uint32_t n, uint32_t sf_id) {
   return (sf_id << 4) | (n >> 3) << 17 | (1u << 23) | ((256u >> 4) << 24) | (sf_id << 29);
+}
+
+// Instruction descriptor for M = 256 (pair), E2M1 x E2M1 (mxf4_idesc gives the
+// fields; M >> 7 = 2 at bits 27-28).
+__host__ __device__ constexpr uint32_t mxf4_idesc_m256(uint32_t n, uint32_t sf_id) {
+  return (sf_id << 4) | (1u << 7) | (1u << 10) | ((n >> 3) << 17) | (1u << 23) | (2u << 27) |
+         (sf_id << 29);
 }
 
 }  // namespace moe

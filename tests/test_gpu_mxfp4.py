@@ -214,6 +214,23 @@ def test_product_whole_numbers_bitwise(counts, behind, N, K, dtype):
         assert torch.equal(p(None, dtype), out)       # one group: offsets not needed
 
 
+# Products large enough for the CTA-pair kernel (224 rows per group, four waves of
+# 256 x 256 tiles): halves of 8 to 128 tokens, an odd number of weight blocks (a
+# pair's second block past N), groups without rows, one K block, several tiles per
+# pair.
+PAIRS = [
+    ([5000], 3, 4104, 32), ([250, 33, 5120, 1, 0], 0, 4096, 96),
+    ([1024, 0, 2050, 255, 17], 7, 6280, 288), ([300] * 10, 0, 7048, 160),
+    ([2000, 31, 32, 33], 0, 10760, 64), ([77000], 0, 136, 32), ([2600, 700], 0, 6152, 1024),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("counts,behind,N,K", PAIRS, ids=[f"q{i}-N{p[2]}-K{p[3]}" for i, p in enumerate(PAIRS)])
+def test_product_on_pairs_whole_numbers_bitwise(counts, behind, N, K, dtype):
+    test_product_whole_numbers_bitwise(counts, behind, N, K, dtype)
+
+
 @pytest.mark.parametrize("counts,behind,N,K", [([5, 40, 0, 9], 0, 264, 2080), ([200, 90], 0, 128, 7168),
                                                ([1], 0, 512, 7168), ([777], 0, 136, 2048),
                                                ([3] * 32, 1, 256, 1536)])
@@ -257,6 +274,61 @@ def test_product_offsets_that_are_not_prefix_sums():
         p.check()
         want = torch.from_numpy(O.grouped_product(av, wv, off, np.full((R, N), 7.0))).bfloat16()
         assert torch.equal(out.cpu(), want), off
+
+
+def test_product_on_pairs_offsets_and_nan_rows():
+    """Offsets that are not prefix sums, and NaN scales, on the CTA-pair kernel."""
+    ensure_built()
+    R, E, N, K = 4000, 4, 5128, 320
+    a, sa, w, sw = _operands(R, E, N, K, 1, whole=True)
+    p = Product(R, E, N, K, a, sa, w, sw)
+    av = O.dequantize_mxfp4(a, sa)
+    wv = O.dequantize_mxfp4(w.reshape(E * N, -1), sw.reshape(E * N, -1)).reshape(E, N, K)
+    for off in ([10, 20, 20, 3900, 3950], [-5, 300, 70, 600, 1 << 30], [4000] * 5,
+                [0, (1 << 31) - 1, 3, 5, 4000]):
+        off = np.array(off, np.int64).astype(np.int32)
+        out = p(_cuda(off), "bf16")
+        p.check()
+        want = torch.from_numpy(O.grouped_product(av, wv, off, np.full((R, N), 7.0))).bfloat16()
+        assert torch.equal(out.cpu(), want), off
+    off = _cuda(_offsets([1000, 1000, 1000, 1000]))
+    clean = p(off, "bf16")
+    sa[2717, 3], sw[1, 130, 9] = 255, 255
+    out = Product(R, E, N, K, a, sa, w, sw)(off, "bf16")
+    want = torch.zeros(R, N, dtype=torch.bool, device="cuda")
+    want[2717], want[1000:2000, 130] = True, True
+    assert torch.equal(torch.isnan(out), want)
+    assert torch.equal(out[~want], clean[~want])
+
+
+def test_product_on_pairs_in_a_graph_beside_another():
+    """A captured pair product (two launches) and a captured small one, workspaces of
+    their own, replayed on two streams at once, equal the eager calls."""
+    ensure_built()
+    cases = [([1500, 2500], 5128, 512), ([40] * 32, 256, 1024)]
+    runs = []
+    for i, (counts, N, K) in enumerate(cases):
+        p = Product(sum(counts), len(counts), N, K, *_operands(sum(counts), len(counts), N, K, 60 + i))
+        off = _cuda(_offsets(counts))
+        want = p(off, "bf16")
+        out = torch.zeros_like(want)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(3):
+                p(off, "bf16", out)
+        runs.append((p, off, want, out, graph, torch.cuda.Stream()))
+    for _ in range(5):
+        for r in runs:
+            r[3].zero_()
+        torch.cuda.synchronize()
+        for r in runs:
+            with torch.cuda.stream(r[5]):
+                r[4].replay()
+        torch.cuda.synchronize()
+        for p, _, want, out, _, _ in runs:
+            assert torch.equal(out, want)
+            p.check()
 
 
 def test_product_keeps_nan_rows_apart():
