@@ -53,11 +53,13 @@ constexpr uint32_t kTmemCols = 512;
 // the smaller tiles cost 10%: the epilogue frees TMEM as soon as it has loaded.)
 constexpr uint32_t kSfCol = 256, kSfSet = 32, kSfTokens = 8;
 
-// kTok: most tokens of a tile.  256: the fewest weight reads per token; 64: twice
-// the stages in flight where an expert has few tokens and the weights stream.
+// kTok: most tokens of a tile.  256: the fewest weight reads per token; 128: half
+// as many stages again where groups have few tokens and the weights stream (with
+// 64, eight stages, one token took 1% less, but a skewed batch of 128 tokens 81 us
+// against 77, reading the weights of its busy experts twice).
 template <int kTok>
 struct Cfg {
-  static constexpr int kStages = kTok == 256 ? 4 : 8;
+  static constexpr int kStages = kTok == 256 ? 4 : 6;
   static constexpr int kBox = kTok == 256 ? 64 : 32;   // rows of a token box
   static constexpr int kChunks = (kTok + 127) / 128;   // 128-row scale chunks
 };
@@ -358,15 +360,18 @@ cudaError_t launch(const MxGemm& p, cudaStream_t st) {
   return launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, map, p);
 }
 
-// Small token tiles (twice the stages) while the average group fits one.
-bool small_tiles(int R, int E) { return R <= 64ll * E; }
-
-// Most tokens of a tile of the large variant.  A K block of a tile of n tokens
-// costs about kBlockClocks + kTokenClocks * n clocks, and a launch as many tiles
-// one after another as there are waves; group sizes are known on the device
-// only, so the groups are taken as equal.
+// Most tokens of a tile.  A K block of a tile of n tokens costs about
+// kBlockClocks + kTokenClocks * n clocks, and a launch as many tiles one after
+// another as there are waves; group sizes are known on the device only, so the
+// groups are taken as equal (one group of 1001 rows, 2080 -> 1544: 104 tiles of 128
+// tokens or 143 of 96 take 7.0 us, 52 of 256 take 9.2).  Several groups with up to
+// kFewRows rows on average get tiles of 128: their sizes scatter, and a group cut in
+// two reads its weights twice (96 rows per group: 92 us against 97 with 256 and four
+// stages; 128 per group: 33 against 31).
 constexpr double kBlockClocks = 300, kTokenClocks = 1.75;
+constexpr long long kFewRows = 96;
 int tile_cap(int R, int E, int nb_n) {
+  if (E > 1 && R <= kFewRows * E) return 128;
   const long long groups = std::min(E, R), rows = (R + groups - 1) / groups;
   const int ctas = sm_count();
   int best = 256;
@@ -376,7 +381,7 @@ int tile_cap(int R, int E, int nb_n) {
     const long long size = ((rows + per - 1) / per + 15) / 16 * 16;
     const double cost =
         static_cast<double>((tiles + ctas - 1) / ctas) * (kBlockClocks + kTokenClocks * size);
-    if (cap == 256 || cost < least) {
+    if (cap == 256 || cost <= least) {
       least = cost;
       best = cap;
     }
@@ -476,18 +481,18 @@ moe_status moe_mxfp4_gemm(const uint8_t* codes, const uint8_t* scales, const int
   p.out = static_cast<uint16_t*>(out);
   p.err = static_cast<uint32_t*>(workspace);
   p.records = static_cast<uint8_t*>(workspace) + 256;
-  const bool small = moe::small_tiles(R, E);
-  p.cap = small ? 64 : moe::tile_cap(R, E, p.nb_n);
+  p.cap = moe::tile_cap(R, E, p.nb_n);
   auto st = reinterpret_cast<cudaStream_t>(stream);
   const bool fp16 = dtype == MOE_T_FP16;
   if (moe::use_pairs(R, E, N)) {
     p.cap = 256;
     return moe::launch_mx_pairs(p, fp16, st) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
   }
-  const cudaError_t e = small ? (fp16 ? moe::launch<64, true>(p, st)
-                                      : moe::launch<64, false>(p, st))
-                              : (fp16 ? moe::launch<256, true>(p, st)
-                                      : moe::launch<256, false>(p, st));
+  cudaError_t e;
+  if (p.cap <= 128)
+    e = fp16 ? moe::launch<128, true>(p, st) : moe::launch<128, false>(p, st);
+  else
+    e = fp16 ? moe::launch<256, true>(p, st) : moe::launch<256, false>(p, st);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
