@@ -286,8 +286,8 @@ moe_status moe_quantize_act(const void *x_bf16, int T, int H, uint8_t *x_codes,
  * of the two.)  Rows are S = T*k rows of H elements in expert order; rows that no slot names --
  * behind the last routed one -- are neither read nor written.  Sums run in
  * fp32, j ascending, and are rounded once to the row type; no atomics, so
- * results repeat bitwise.  An output may not overlap an input
- * (MOE_ERR_INVALID_ARG).  All calls are one launch on `stream`, can be captured
+ * results repeat bitwise.  An output may overlap neither an input nor another
+ * output (MOE_ERR_INVALID_ARG; the MXFP4 calls too).  All calls are one launch on `stream`, can be captured
  * into a graph, and may run concurrently with one another.
  * T >= 1, k >= 1 (k may exceed the layer's 256 experts), T*k < 2^31; rows of a
  * multiple of 16 bytes (MOE_ERR_UNSUPPORTED otherwise).                      */
@@ -330,7 +330,7 @@ moe_status moe_unpermute_backward(const void *dout, const void *rows, int dtype,
 
 /* ---- MXFP4: E2M1 codes with one UE8M0 scale per 32 elements of a row. -------
  * Codes are u8 [R, K/2], element 2i in the low nibble of byte i; K % 32 == 0,
- * K <= 2^30.
+ * K <= 2^28.
  * Scale bytes come in one of two layouts:
  *   MOE_SCALES_ROW_MAJOR    u8 [R, K/32], the layout of the layer's MXFP4 weights
  *   MOE_SCALES_GROUP_MAJOR  u8 [ceil(K/128), R, 4]: byte (g, r, j) scales row r's

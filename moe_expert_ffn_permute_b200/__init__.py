@@ -434,6 +434,8 @@ def _buf(fn, name, t, nbytes, dtype, device):
     for it), and so is None (the library refuses it where it is required)."""
     if t is None or isinstance(t, int):
         return t
+    if not hasattr(t, "data_ptr"):
+        raise TypeError(f"{fn}: {name}: expected an address or a tensor, got {type(t)}")
     want = _TYPE[dtype]
     if (t.get_device() == device and t.is_contiguous() and (want is None or t.dtype is want)
             and t.nbytes >= nbytes):

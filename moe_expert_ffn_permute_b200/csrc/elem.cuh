@@ -62,13 +62,27 @@ inline bool elem_ok(int dtype) {
   return dtype == MOE_T_BF16 || dtype == MOE_T_FP16 || dtype == MOE_T_FP32;
 }
 
-// Whether two buffers share a byte (a null buffer shares none).  The row
-// operators read through the read-only path and in no set order, so an output
-// may not lie in an input.
-inline bool buffers_overlap(const void* a, long long a_bytes, const void* b, long long b_bytes) {
-  const auto x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  if (x == 0 || y == 0) return false;
-  return x < y + static_cast<uintptr_t>(b_bytes) && y < x + static_cast<uintptr_t>(a_bytes);
+// A buffer of a call.  The operators read through the read-only path and in no
+// set order, so an output may lie neither in an input nor in another output.
+struct Buffer {
+  const void* p;
+  long long bytes;
+  bool out;
+};
+
+// Whether an output shares a byte with another buffer (a null one shares none).
+template <int kN>
+inline bool outputs_overlap(const Buffer (&b)[kN]) {
+  for (int i = 0; i < kN; ++i)
+    for (int j = i + 1; j < kN; ++j) {
+      if ((!b[i].out && !b[j].out) || b[i].p == nullptr || b[j].p == nullptr) continue;
+      const auto x = reinterpret_cast<uintptr_t>(b[i].p), y = reinterpret_cast<uintptr_t>(b[j].p);
+      if (x < y + static_cast<uintptr_t>(b[j].bytes) && y < x + static_cast<uintptr_t>(b[i].bytes))
+        return true;
+    }
+  return false;
 }
+
+inline bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 }  // namespace moe

@@ -24,7 +24,7 @@ constexpr int kThreads = 256;
 constexpr int kSlotGroup = 8;    // slots whose stores are issued together
 constexpr int kUnit = 16;        // elements a thread owns: half a block
 constexpr int kGroupUnits = 8;   // threads of a 128-wide group (four blocks)
-constexpr int kMaxRow = 1 << 30; // elements of a row (K rounded up still fits an int)
+constexpr int kMaxRow = 1 << 28; // elements of a row (bytes of 2^31 rows fit 64 bits)
 
 // UE8M0 byte of a block from the largest magnitude's fp32 bits: 6 = 1.5 * 2^2,
 // so with amax = m * 2^e, m in [1, 2), n = e - 2 if m <= 1.5, else e - 1.
@@ -313,8 +313,6 @@ __global__ void __launch_bounds__(kThreads) prepack_mxfp4_scales_kernel(
   }
 }
 
-bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-
 bool layout_ok(int layout) {
   return layout == MOE_SCALES_ROW_MAJOR || layout == MOE_SCALES_GROUP_MAJOR;
 }
@@ -390,9 +388,9 @@ moe_status moe_quantize_mxfp4(const void* x, int dtype, int T, int K, int k, con
   const long long R = static_cast<long long>(T) * k;
   const long long xb = static_cast<long long>(T) * K * moe::elem_bytes(dtype), cb = R * (K / 2);
   const long long sb = moe::scale_bytes(R, K, scale_layout);
-  if (moe::buffers_overlap(x, xb, codes, cb) || moe::buffers_overlap(x, xb, scales, sb) ||
-      moe::buffers_overlap(codes, cb, scales, sb))
-    return MOE_ERR_INVALID_ARG;
+  const moe::Buffer buffers[] = {
+      {x, xb, false}, {inv, R * 4, false}, {codes, cb, true}, {scales, sb, true}};
+  if (moe::outputs_overlap(buffers)) return MOE_ERR_INVALID_ARG;
   const unsigned blocks = moe::blocks_of(T * ((K + 127ll) / 128) * moe::kGroupUnits);
   if (blocks == 0) return MOE_ERR_UNSUPPORTED;
   auto launch = dtype == MOE_T_BF16   ? moe::launch_quantize<MOE_T_BF16>
@@ -412,10 +410,10 @@ moe_status moe_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, int
   if (K % 32 != 0 || K > moe::kMaxRow) return MOE_ERR_UNSUPPORTED;
   if (!moe::aligned_to(codes, 16) || !moe::aligned_to(out, 32)) return MOE_ERR_ALIGNMENT;
   const long long n = R * static_cast<long long>(K);
-  if (moe::buffers_overlap(codes, n / 2, out, n * moe::elem_bytes(dtype)) ||
-      moe::buffers_overlap(scales, moe::scale_bytes(R, K, scale_layout), out,
-                           n * moe::elem_bytes(dtype)))
-    return MOE_ERR_INVALID_ARG;
+  const moe::Buffer buffers[] = {{codes, n / 2, false},
+                                 {scales, moe::scale_bytes(R, K, scale_layout), false},
+                                 {out, n * moe::elem_bytes(dtype), true}};
+  if (moe::outputs_overlap(buffers)) return MOE_ERR_INVALID_ARG;
   if (n / moe::kUnit > (1ll << 38)) return MOE_ERR_UNSUPPORTED;   // the grid's limit
   auto launch = dtype == MOE_T_BF16   ? moe::launch_dequantize<MOE_T_BF16>
                 : dtype == MOE_T_FP16 ? moe::launch_dequantize<MOE_T_FP16>
@@ -444,14 +442,11 @@ moe_status moe_mxfp4_prepack(const uint8_t* w, const uint8_t* w_scales, int E, i
       !moe::aligned_to(w_scales_chunked, 16))
     return MOE_ERR_ALIGNMENT;
   const long long rows = static_cast<long long>(E) * N;
-  const struct { const void* p; long long n; bool out; } buf[4] = {
-      {w, rows * (K / 2), false}, {w_scales, rows * (K / 32), false},
-      {w_tiled, tiles * static_cast<long long>(moe::kTileBytes), true},
-      {w_scales_chunked, tiles * 1024, true}};
-  for (int a = 0; a < 4; ++a)
-    for (int b = a + 1; b < 4; ++b)
-      if (buf[b].out && moe::buffers_overlap(buf[a].p, buf[a].n, buf[b].p, buf[b].n))
-        return MOE_ERR_INVALID_ARG;
+  const moe::Buffer buffers[] = {{w, rows * (K / 2), false},
+                                 {w_scales, rows * (K / 32), false},
+                                 {w_tiled, tiles * static_cast<long long>(moe::kTileBytes), true},
+                                 {w_scales_chunked, tiles * 1024, true}};
+  if (moe::outputs_overlap(buffers)) return MOE_ERR_INVALID_ARG;
   auto st = reinterpret_cast<cudaStream_t>(stream);
   const unsigned most = static_cast<unsigned>(moe::sm_count()) * 16;
   const long long cb = tiles * static_cast<long long>(moe::kTileBytes / 16) / moe::kThreads;

@@ -399,8 +399,6 @@ bool use_pairs(int R, int E, int N) {
   return R >= 224ll * E && (R / 256) * ((N + 255ll) / 256) >= 2ll * sm_count();
 }
 
-bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-
 }  // namespace
 
 bool mx::map_rows(CUtensorMap* m, const void* base, uint64_t width, uint64_t rows, uint32_t box,
@@ -463,9 +461,16 @@ moe_status moe_mxfp4_gemm(const uint8_t* codes, const uint8_t* scales, const int
       !moe::aligned_to(workspace, 256))
     return MOE_ERR_ALIGNMENT;
   const long long rb = R;
-  if (moe::buffers_overlap(out, rb * N * 2, codes, rb * (K / 2)) ||
-      moe::buffers_overlap(out, rb * N * 2, scales, (K + 127) / 128 * rb * 4))
-    return MOE_ERR_INVALID_ARG;
+  const long long tiles = static_cast<long long>(E) * ((N + 127) / 128) * ((K + 255) / 256);
+  const moe::Buffer buffers[] = {
+      {codes, rb * (K / 2), false},
+      {scales, (K + 127) / 128 * rb * 4, false},
+      {offsets, (E + 1) * 4ll, false},
+      {w_tiled, tiles * static_cast<long long>(moe::kTileBytes), false},
+      {w_scales_chunked, tiles * 1024, false},
+      {out, rb * N * 2, true},
+      {workspace, static_cast<long long>(moe_mxfp4_workspace_bytes(R, E, N, K)), true}};
+  if (moe::outputs_overlap(buffers)) return MOE_ERR_INVALID_ARG;
   moe::MxGemm p{};
   p.R = R;
   p.E = E;

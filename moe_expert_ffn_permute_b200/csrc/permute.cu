@@ -191,13 +191,11 @@ __global__ void __launch_bounds__(kThreads) unpermute_backward_kernel(
   }
 }
 
-bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
-
 // Blocks of kThreads for one thread per (token, pair of chunks); 0 if the grid
-// would exceed its limit.
-unsigned copy_blocks(int T, long long vecs) {
+// would exceed its limit, or the rows' bytes 64 bits.
+unsigned copy_blocks(int T, long long vecs, int k) {
   const long long half = (vecs + kCpt - 1) / kCpt;
-  if (half > (1ll << 62) / T) return 0;
+  if (vecs > (1ll << 58) / T / k) return 0;
   const long long blocks = (T * half + kThreads - 1) / kThreads;
   return blocks < (1ll << 31) ? static_cast<unsigned>(blocks) : 0u;
 }
@@ -206,7 +204,8 @@ unsigned copy_blocks(int T, long long vecs) {
 moe_status check_rows(int dtype, int T, int H, int k) {
   if (!elem_ok(dtype) || T < 1 || H < 1 || k < 1) return MOE_ERR_INVALID_ARG;
   if (static_cast<long long>(T) * k >= (1ll << 31)) return MOE_ERR_INVALID_ARG;
-  if (static_cast<long long>(H) * elem_bytes(dtype) % 16 != 0) return MOE_ERR_UNSUPPORTED;
+  const long long row_bytes = static_cast<long long>(H) * elem_bytes(dtype);
+  if (row_bytes % 16 != 0 || copy_blocks(T, row_bytes / 16, k) == 0) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -215,14 +214,17 @@ moe_status sum_rows(const void* rows, int dtype, int T, int H, int k, const int3
   if (rows == nullptr || inv == nullptr || out == nullptr) return MOE_ERR_INVALID_ARG;
   const moe_status s = check_rows(dtype, T, H, k);
   if (s != MOE_OK) return s;
-  if (!aligned16(rows) || !aligned16(out) || reinterpret_cast<uintptr_t>(inv) % 4 != 0 ||
-      reinterpret_cast<uintptr_t>(topk_w) % 4 != 0)
+  if (!aligned_to(rows, 16) || !aligned_to(out, 16) || !aligned_to(inv, 4) ||
+      !aligned_to(topk_w, 4))
     return MOE_ERR_ALIGNMENT;
   const long long vecs = static_cast<long long>(H) * elem_bytes(dtype) / 16;
-  const unsigned blocks = copy_blocks(T, vecs);
-  if (blocks == 0) return MOE_ERR_UNSUPPORTED;
+  const unsigned blocks = copy_blocks(T, vecs, k);
   const long long S = static_cast<long long>(T) * k;
-  if (buffers_overlap(rows, S * vecs * 16, out, T * vecs * 16)) return MOE_ERR_INVALID_ARG;
+  const Buffer buffers[] = {{rows, S * vecs * 16, false},
+                            {inv, S * 4, false},
+                            {topk_w, S * 4, false},
+                            {out, T * vecs * 16, true}};
+  if (outputs_overlap(buffers)) return MOE_ERR_INVALID_ARG;
   auto kern = dtype == MOE_T_BF16   ? unpermute_kernel<MOE_T_BF16>
               : dtype == MOE_T_FP16 ? unpermute_kernel<MOE_T_FP16>
                                     : unpermute_kernel<MOE_T_FP32>;
@@ -270,8 +272,6 @@ cudaError_t launch_backward_any(const void* dout, const void* rows, const int32_
 }  // namespace
 }  // namespace moe
 
-using moe::aligned16;
-
 extern "C" {
 
 moe_status moe_permute(const void* x, int T, int64_t row_bytes, int k, const int32_t* inv,
@@ -280,17 +280,19 @@ moe_status moe_permute(const void* x, int T, int64_t row_bytes, int k, const int
   if (T < 1 || row_bytes < 1 || k < 1 || static_cast<long long>(T) * k >= (1ll << 31))
     return MOE_ERR_INVALID_ARG;
   if (row_bytes % 4 != 0) return MOE_ERR_UNSUPPORTED;
-  if (!aligned16(x) || !aligned16(rows) || reinterpret_cast<uintptr_t>(inv) % 4 != 0)
+  if (!moe::aligned_to(x, 16) || !moe::aligned_to(rows, 16) || !moe::aligned_to(inv, 4))
     return MOE_ERR_ALIGNMENT;
   auto st = reinterpret_cast<cudaStream_t>(stream);
   // Rows of whole 16-byte vectors keep every row 16-byte aligned; others
   // (scale bytes of odd sizes) go word by word.
   const bool wide = row_bytes % 16 == 0;
   const long long vecs = row_bytes / (wide ? 16 : 4);
-  const unsigned blocks = moe::copy_blocks(T, vecs);
+  const unsigned blocks = moe::copy_blocks(T, vecs, k);
   if (blocks == 0) return MOE_ERR_UNSUPPORTED;
-  if (moe::buffers_overlap(x, T * row_bytes, rows, static_cast<long long>(T) * k * row_bytes))
-    return MOE_ERR_INVALID_ARG;
+  const long long S = static_cast<long long>(T) * k;
+  const moe::Buffer buffers[] = {
+      {x, T * row_bytes, false}, {inv, S * 4, false}, {rows, S * row_bytes, true}};
+  if (moe::outputs_overlap(buffers)) return MOE_ERR_INVALID_ARG;
   const cudaError_t e =
       wide ? moe::launch_pdl(moe::permute_kernel<uint4>, dim3(blocks), dim3(moe::kThreads), 0, st,
                              static_cast<const uint4*>(x), inv, T, vecs, k,
@@ -320,18 +322,18 @@ moe_status moe_unpermute_backward(const void* dout, const void* rows, int dtype,
   if (dw != nullptr && rows == nullptr) return MOE_ERR_INVALID_ARG;
   const moe_status s = moe::check_rows(dtype, T, H, k);
   if (s != MOE_OK) return s;
-  if (!aligned16(dout) || !aligned16(rows) || !aligned16(drows) ||
-      reinterpret_cast<uintptr_t>(inv) % 4 != 0 || reinterpret_cast<uintptr_t>(topk_w) % 4 != 0 ||
-      reinterpret_cast<uintptr_t>(dw) % 4 != 0)
+  if (!moe::aligned_to(dout, 16) || !moe::aligned_to(rows, 16) || !moe::aligned_to(drows, 16) ||
+      !moe::aligned_to(inv, 4) || !moe::aligned_to(topk_w, 4) || !moe::aligned_to(dw, 4))
     return MOE_ERR_ALIGNMENT;
   const long long vecs = static_cast<long long>(H) * moe::elem_bytes(dtype) / 16;
   const long long S = static_cast<long long>(T) * k;
-  if (moe::buffers_overlap(drows, S * vecs * 16, dout, T * vecs * 16) ||
-      moe::buffers_overlap(drows, S * vecs * 16, dw != nullptr ? rows : nullptr, S * vecs * 16) ||
-      moe::buffers_overlap(dw, S * 4, dout, T * vecs * 16) ||
-      moe::buffers_overlap(dw, S * 4, rows, S * vecs * 16) ||
-      moe::buffers_overlap(dw, S * 4, drows, S * vecs * 16))
-    return MOE_ERR_INVALID_ARG;
+  const moe::Buffer buffers[] = {{dout, T * vecs * 16, false},
+                                 {dw != nullptr ? rows : nullptr, S * vecs * 16, false},
+                                 {inv, S * 4, false},
+                                 {topk_w, S * 4, false},
+                                 {drows, S * vecs * 16, true},
+                                 {dw, S * 4, true}};
+  if (moe::outputs_overlap(buffers)) return MOE_ERR_INVALID_ARG;
   auto st = reinterpret_cast<cudaStream_t>(stream);
   auto launch = dtype == MOE_T_BF16   ? moe::launch_backward_any<MOE_T_BF16>
                 : dtype == MOE_T_FP16 ? moe::launch_backward_any<MOE_T_FP16>

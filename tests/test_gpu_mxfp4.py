@@ -460,3 +460,74 @@ def test_tensor_checks_on_the_gpu():
         with pytest.raises(moe.MoEError) as e:
             moe.moe_mxfp4_gemm(**{**args, **over})
         assert e.value.status == moe.MOE_ERR_INVALID_ARG, over
+
+
+def test_buffers_at_the_least_alignment():
+    """Codes 16, scales and offsets 4, quantiser inputs 32 bytes off a larger
+    boundary give the same bytes."""
+    from test_gpu_rows import _at
+    ensure_built()
+    T, K, k, E, N = 29, 352, 3, 4, 136
+    g = _gen(51)
+    inv, offsets = _route(T, k, E, 0.1, g)
+    S = T * k
+    x = _hard(T, K, "bf16", 8)
+    x = torch.where(torch.isfinite(x.float()) & (x.float().abs() < 1e4), x, 1.0)
+    w = torch.randint(0, 256, (E, N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    ws = torch.randint(120, 128, (E, N, K // 32), generator=g, device="cuda", dtype=torch.uint8)
+
+    def run(make):
+        a, iv, off = (make(32, x.shape, x.dtype, x), make(4, inv.shape, inv.dtype, inv),
+                      make(12, offsets.shape, offsets.dtype, offsets))
+        codes = make(16, (S, K // 2), torch.uint8)
+        scales = make(4, moe.mxfp4_scale_shape(S, K, "group"), torch.uint8)
+        moe.moe_quantize_mxfp4(a, "bf16", T, K, k, iv, codes, scales, "group")
+        val = make(32, (S, K), torch.float32)
+        moe.moe_dequantize_mxfp4(codes, scales, "group", S, K, "fp32", val)
+        wt = make(16, (moe.moe_mxfp4_weight_bytes(E, N, K),), torch.uint8)
+        st = make(48, (moe.moe_mxfp4_weight_scale_bytes(E, N, K),), torch.uint8)
+        moe.moe_mxfp4_prepack(make(16, w.shape, w.dtype, w), make(1, ws.shape, ws.dtype, ws), E, N, K, wt, st)
+        out = make(16, (S, N), torch.bfloat16)
+        space = torch.zeros(moe.moe_mxfp4_workspace_bytes(S, E, N, K), dtype=torch.uint8, device="cuda")
+        moe.moe_mxfp4_gemm(codes, scales, off, S, E, N, K, wt, st, "bf16", out, space)
+        assert moe.moe_mxfp4_check_error(space) == 0
+        return codes, scales, val, out
+
+    plain = run(lambda off, shape, dt, fill=None: torch.zeros(shape, dtype=dt, device="cuda")
+                if fill is None else fill.clone())
+    for a, b in zip(run(_at), plain):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("R,E,N,K", [(300000, 2, 8192, 64), (56000, 256, 40960, 32), (1100000, 1, 8, 8192)],
+                         ids=["pairs-out", "single-out", "codes"])
+def test_product_offsets_past_32_bits(R, E, N, K):
+    """Outputs or codes of more than 2^32 bytes, on both kernels; rows from every
+    part of the range against the oracle, bitwise (whole-number operands)."""
+    ensure_built()
+    g = _gen(R)
+    rnd = lambda *s: torch.randint(0, 256, s, generator=g, device="cuda", dtype=torch.uint8)  # noqa: E731
+    codes, w = rnd(R, K // 2), rnd(E, N, K // 2)
+    if K > 1024:       # sparse rows: the sums stay within 24 bits
+        codes[:, 16:] = 0
+        codes[:, -16:] = rnd(R, 16)
+    one = lambda *s: torch.full(s, 127, dtype=torch.uint8, device="cuda")  # noqa: E731
+    scales, ws = one((K + 127) // 128, R, 4), one(E, N, K // 32)
+    if K % 128:
+        scales[-1, :, (K % 128) // 32:] = 0
+    cut = np.sort(np.random.default_rng(R).integers(0, R, E - 1))
+    off = np.concatenate([[0], cut, [R]]).astype(np.int32)
+    p = Product.__new__(Product)
+    p.R, p.E, p.N, p.K, p.codes, p.scales = R, E, N, K, codes, scales
+    p.w = torch.empty(moe.moe_mxfp4_weight_bytes(E, N, K), dtype=torch.uint8, device="cuda")
+    p.ws = torch.empty(moe.moe_mxfp4_weight_scale_bytes(E, N, K), dtype=torch.uint8, device="cuda")
+    moe.moe_mxfp4_prepack(w, ws, E, N, K, p.w, p.ws)
+    p.workspace = torch.zeros(moe.moe_mxfp4_workspace_bytes(R, E, N, K), dtype=torch.uint8, device="cuda")
+    out = torch.empty(R, N, dtype=torch.bfloat16, device="cuda")
+    p(_cuda(off), "bf16", out)
+    p.check()
+    for r in [0, 1, R // 3, R // 2 + 7, R - 300, R - 2, R - 1]:
+        e = int(np.searchsorted(off, r, side="right")) - 1
+        a = O.dequantize_mxfp4(codes[r:r + 1].cpu().numpy(), np.full((1, K // 32), 127, np.uint8))
+        b = O.dequantize_mxfp4(w[e].cpu().numpy(), np.full((N, K // 32), 127, np.uint8))
+        assert torch.equal(out[r].cpu(), torch.from_numpy((a @ b.T)[0]).bfloat16()), r

@@ -291,3 +291,73 @@ def test_tensor_checks_on_the_gpu():
         with pytest.raises(moe.MoEError) as e:
             call()
         assert e.value.status == moe.MOE_ERR_INVALID_ARG
+
+
+def _at(offset, shape, dtype, fill=None):
+    """A contiguous tensor `offset` bytes into an allocation (512-byte aligned)."""
+    n = int(np.prod(shape)) * torch.empty((), dtype=dtype).element_size()
+    base = torch.zeros(n + 1024, dtype=torch.uint8, device="cuda")
+    t = base[offset:offset + n].view(dtype).view(shape)
+    assert t.data_ptr() % 512 == offset and t.is_contiguous()
+    if fill is not None:
+        t.copy_(fill)
+    return t
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_buffers_at_the_least_alignment(dtype):
+    """Rows 16 bytes and indices 4 bytes off a larger boundary give the same bytes."""
+    ensure_built()
+    T, H, k, E = 45, 264, 5, 8
+    g = _gen(31)
+    inv, _ = _route(T, k, E, 0.1, g)
+    x = torch.randn(T, H, generator=g, device="cuda").to(DT[dtype])
+    w = torch.randn(T, k, generator=g, device="cuda")
+    dout = torch.randn(T, H, generator=g, device="cuda").to(DT[dtype])
+
+    def run(make):
+        a, iv, wt, do = (make(16, x.shape, x.dtype, x), make(4, inv.shape, inv.dtype, inv),
+                         make(12, w.shape, w.dtype, w), make(48, dout.shape, dout.dtype, dout))
+        rows, out = make(80, (T * k, H), x.dtype), make(16, (T, H), x.dtype)
+        drows, dw, dx = make(112, (T * k, H), x.dtype), make(20, (T, k), torch.float32), make(16, (T, H), x.dtype)
+        moe.moe_permute(a, T, H * x.element_size(), k, iv, rows)
+        moe.moe_unpermute(rows, dtype, T, H, k, iv, wt, out)
+        moe.moe_unpermute_backward(do, rows, dtype, T, H, k, iv, wt, drows, dw)
+        moe.moe_permute_backward(drows, dtype, T, H, k, iv, dx)
+        return rows, out, drows, dw, dx
+
+    plain = run(lambda off, shape, dt, fill=None: torch.zeros(shape, dtype=dt, device="cuda")
+                if fill is None else fill.clone())
+    for a, b in zip(run(_at), plain):
+        assert torch.equal(a, b)
+
+
+def test_two_calls_at_once():
+    """The same operators on two streams at once, on shared inputs."""
+    ensure_built()
+    T, H, k, E = 700, 2048, 6, 32
+    g = _gen(41)
+    inv, _ = _route(T, k, E, 0.05, g)
+    x = torch.randn(T, H, generator=g, device="cuda").to(torch.bfloat16)
+    w = torch.randn(T, k, generator=g, device="cuda")
+    bufs = []
+    for _ in range(3):
+        bufs.append([torch.zeros(T * k, H, dtype=x.dtype, device="cuda"), torch.zeros_like(x),
+                     torch.zeros(T * k, H, dtype=x.dtype, device="cuda"), torch.zeros_like(w)])
+    torch.cuda.synchronize()
+
+    def run(b):
+        moe.moe_permute(x, T, H * 2, k, inv, b[0])
+        moe.moe_unpermute(b[0], "bf16", T, H, k, inv, w, b[1])
+        moe.moe_unpermute_backward(x, b[0], "bf16", T, H, k, inv, w, b[2], b[3])
+
+    run(bufs[0])
+    torch.cuda.synchronize()
+    for _ in range(10):
+        streams = [torch.cuda.Stream() for _ in range(2)]
+        for s, b in zip(streams, bufs[1:]):
+            with torch.cuda.stream(s):
+                run(b)
+        torch.cuda.synchronize()
+        for b in bufs[1:]:
+            assert all(torch.equal(p, q) for p, q in zip(b, bufs[0]))

@@ -66,6 +66,15 @@ CASES = [
     ("moe_unpermute_backward", INVALID, dict(dw=E_ + 16)),
     ("moe_unpermute_backward", ALIGNMENT, dict(dw=F_ + 2)),
     ("moe_unpermute_backward", UNSUPPORTED, dict(H=20)),
+    ("moe_permute", INVALID, dict(rows=B)), ("moe_permute", UNSUPPORTED, dict(T=1, k=(1 << 31) - 1, row_bytes=1 << 40)),
+    ("moe_unpermute", INVALID, dict(out=C)), ("moe_unpermute", INVALID, dict(out=B + 16)),
+    ("moe_unpermute_backward", INVALID, dict(dw=D)), ("moe_unpermute_backward", INVALID, dict(dw=C)),
+    ("moe_unpermute_backward", INVALID, dict(drows=C)),
+    ("moe_unpermute_backward", INVALID, dict(drows=D, dw=None)),
+    ("moe_quantize_mxfp4", INVALID, dict(codes=B)), ("moe_quantize_mxfp4", INVALID, dict(scales=B)),
+    ("moe_mxfp4_gemm", INVALID, dict(out=C)), ("moe_mxfp4_gemm", INVALID, dict(out=D)),
+    ("moe_mxfp4_gemm", INVALID, dict(out=E_)), ("moe_mxfp4_gemm", INVALID, dict(out=G)),
+    ("moe_mxfp4_gemm", INVALID, dict(workspace=A)),
     ("moe_quantize_mxfp4", INVALID, dict(inv=None)), ("moe_quantize_mxfp4", INVALID, dict(x=None)),
     ("moe_quantize_mxfp4", INVALID, dict(scale_layout="col")),
     ("moe_quantize_mxfp4", INVALID, dict(T=0)), ("moe_quantize_mxfp4", INVALID, dict(codes=A)),
@@ -74,9 +83,9 @@ CASES = [
     ("moe_quantize_mxfp4", ALIGNMENT, dict(scales=D + 2)),
     ("moe_quantize_mxfp4", ALIGNMENT, dict(codes=C + 8)),
     ("moe_quantize_mxfp4", ALIGNMENT, dict(x=A + 16)),
-    ("moe_quantize_mxfp4", UNSUPPORTED, dict(T=1, k=1, inv=None, K=(1 << 30) + 32)),
+    ("moe_quantize_mxfp4", UNSUPPORTED, dict(T=1, k=1, inv=None, K=(1 << 28) + 32)),
     ("moe_dequantize_mxfp4", ALIGNMENT, dict(out=C + 16)),
-    ("moe_dequantize_mxfp4", UNSUPPORTED, dict(R=1, K=(1 << 30) + 32)),
+    ("moe_dequantize_mxfp4", UNSUPPORTED, dict(R=1, K=(1 << 28) + 32)),
     ("moe_dequantize_mxfp4", INVALID, dict(R=0)), ("moe_dequantize_mxfp4", INVALID, dict(out=A)),
     ("moe_dequantize_mxfp4", INVALID, dict(out=B)), ("moe_dequantize_mxfp4", INVALID, dict(scales=None)),
     ("moe_dequantize_mxfp4", UNSUPPORTED, dict(K=16)),
@@ -108,6 +117,12 @@ def test_tensors_on_the_cpu_are_refused():
     _refused(INVALID, "moe_unpermute", out=x)
     _refused(INVALID, "moe_quantize_mxfp4", x=x)
     _refused(INVALID, "moe_mxfp4_gemm", codes=torch.zeros(8, 32, dtype=torch.uint8))
+
+
+def test_other_objects_are_a_type_error():
+    import numpy as np
+    with pytest.raises(TypeError):
+        moe.moe_permute(np.zeros(4), 1, 16, 1, B, C, stream=0)
 
 
 def test_sizes_that_do_not_fit_are_refused():
