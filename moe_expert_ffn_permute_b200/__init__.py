@@ -128,31 +128,48 @@ def _ptr(v):
     raise TypeError(f"expected an address or a tensor, got {type(v)}")
 
 
-_raw_stream = None
+_current_device = None   # torch.cuda.current_device once CUDA is known to be there
+_raw_stream = None       # device index -> handle of its current stream
+_TYPE = {}               # names of _buf's types -> torch dtypes
+
+
+def _find_cuda():
+    """Looks CUDA up in torch, once; False without it (the next call looks again)."""
+    global _current_device, _raw_stream
+    if _current_device is not None:
+        return True
+    try:
+        import torch
+    except ImportError:  # pragma: no cover
+        return False
+    _TYPE.update(i32=torch.int32, f32=torch.float32, u8=torch.uint8, bf16=torch.bfloat16,
+                 fp16=torch.float16, fp32=torch.float32, any=None)
+    if not torch.cuda.is_available():
+        return False
+    # The current stream's handle without a Stream object around it (0.2 us a
+    # call against 3 us for current_stream().cuda_stream).
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if _raw_stream is None:  # pragma: no cover
+        _raw_stream = lambda device: torch.cuda.current_stream(device).cuda_stream  # noqa: E731
+    _current_device = torch.cuda.current_device
+    return True
 
 
 def _stream(s):
     if s is None:
-        global _raw_stream
-        if _raw_stream is None:
-            try:
-                import torch
-            except ImportError:  # pragma: no cover
-                return None
-            if not torch.cuda.is_available():
-                return None
-            # The current stream's handle without a Stream object around it
-            # (0.3 us a call against 3.2 us for current_stream().cuda_stream).
-            device = torch.cuda.current_device
-            raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-            if raw is not None:
-                _raw_stream = lambda: raw(device())  # noqa: E731
-            else:  # pragma: no cover
-                _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
-        return _raw_stream()
+        return _raw_stream(_current_device()) if _find_cuda() else None
     if isinstance(s, int):
         return s
     return s.cuda_stream
+
+
+def _here(stream):
+    """The current device's index (-2 without CUDA: no tensor is on it) and the
+    handle of `stream` (None: its current stream)."""
+    if _current_device is None and not _find_cuda():
+        return -2, _stream(stream)
+    device = _current_device()
+    return device, _raw_stream(device) if stream is None else _stream(stream)
 
 
 def _check(status, what):
@@ -409,37 +426,23 @@ def _choice(fn, name, table, value):
 
 
 _ELEM = {"bf16": 2, "fp16": 2, "fp32": 4}     # bytes per element
-_current_device = None
-_TYPE = {}                                     # name -> torch dtype
-
-
-def _device():
-    """The current CUDA device's index (-2 without CUDA: no tensor is on it)."""
-    global _current_device
-    if _current_device is None:
-        import torch
-        _TYPE.update(i32=torch.int32, f32=torch.float32, u8=torch.uint8, bf16=torch.bfloat16,
-                     fp16=torch.float16, fp32=torch.float32, any=None)
-        if not torch.cuda.is_available():
-            return -2
-        _current_device = torch.cuda.current_device
-    return _current_device()
 
 
 def _buf(fn, name, t, nbytes, dtype, device):
     """Address of one buffer of a call: a tensor, an address or None.  The C ABI
     sees only pointers, so a tensor is checked here: contiguous, on the current
-    CUDA device (`device`, from _device()), of type `dtype` (a key of _TYPE) and
+    CUDA device (`device`, from _here()), of type `dtype` (a key of _TYPE) and
     at least `nbytes` long.  A raw address is passed through (the caller vouches
     for it), and so is None (the library refuses it where it is required)."""
     if t is None or isinstance(t, int):
         return t
-    if not hasattr(t, "data_ptr"):
-        raise TypeError(f"{fn}: {name}: expected an address or a tensor, got {type(t)}")
-    want = _TYPE[dtype]
-    if (t.get_device() == device and t.is_contiguous() and (want is None or t.dtype is want)
-            and t.nbytes >= nbytes):
-        return t.data_ptr()
+    try:
+        want = _TYPE[dtype]
+        if (t.get_device() == device and t.is_contiguous() and (want is None or t.dtype is want)
+                and t.nbytes >= nbytes):
+            return t.data_ptr()
+    except AttributeError:
+        raise TypeError(f"{fn}: {name}: expected an address or a tensor, got {type(t)}") from None
     if t.get_device() != device:
         what = f"must be on the current CUDA device, is on {t.device}"
     elif not t.is_contiguous():
@@ -455,10 +458,11 @@ def moe_permute(x, T, row_bytes, k, inv, rows, stream=None):
     """rows[inv[t, j]] = x[t]: x [T, row_bytes] of any type -> rows [T*k, row_bytes]."""
     fn = "moe_permute"
     _sizes(fn, T, k)
-    S, at = T * k, _device()
+    S = T * k
+    at, st = _here(stream)
     _check(lib().moe_permute(_buf(fn, "x", x, T * row_bytes, "any", at), T, row_bytes, k,
                              _buf(fn, "inv", inv, 4 * S, "i32", at),
-                             _buf(fn, "rows", rows, S * row_bytes, "any", at), _stream(stream)), fn)
+                             _buf(fn, "rows", rows, S * row_bytes, "any", at), st), fn)
 
 
 def moe_permute_backward(drows, dtype, T, H, k, inv, dx, stream=None):
@@ -466,11 +470,12 @@ def moe_permute_backward(drows, dtype, T, H, k, inv, dx, stream=None):
     fn = "moe_permute_backward"
     d = _choice(fn, "dtype", DTYPES, dtype)
     _sizes(fn, T, H, k)
-    z, at = _ELEM[dtype], _device()
+    z = _ELEM[dtype]
+    at, st = _here(stream)
     S = T * k
     _check(lib().moe_permute_backward(_buf(fn, "drows", drows, S * H * z, dtype, at), d, T, H, k,
                                       _buf(fn, "inv", inv, 4 * S, "i32", at),
-                                      _buf(fn, "dx", dx, T * H * z, dtype, at), _stream(stream)), fn)
+                                      _buf(fn, "dx", dx, T * H * z, dtype, at), st), fn)
 
 
 def moe_unpermute(rows, dtype, T, H, k, inv, topk_w, out, stream=None):
@@ -478,12 +483,13 @@ def moe_unpermute(rows, dtype, T, H, k, inv, topk_w, out, stream=None):
     fn = "moe_unpermute"
     d = _choice(fn, "dtype", DTYPES, dtype)
     _sizes(fn, T, H, k)
-    z, at = _ELEM[dtype], _device()
+    z = _ELEM[dtype]
+    at, st = _here(stream)
     S = T * k
     _check(lib().moe_unpermute(_buf(fn, "rows", rows, S * H * z, dtype, at), d, T, H, k,
                                _buf(fn, "inv", inv, 4 * S, "i32", at),
                                _buf(fn, "topk_w", topk_w, 4 * S, "f32", at),
-                               _buf(fn, "out", out, T * H * z, dtype, at), _stream(stream)), fn)
+                               _buf(fn, "out", out, T * H * z, dtype, at), st), fn)
 
 
 def moe_unpermute_backward(dout, rows, dtype, T, H, k, inv, topk_w, drows, dw, stream=None):
@@ -492,13 +498,14 @@ def moe_unpermute_backward(dout, rows, dtype, T, H, k, inv, topk_w, drows, dw, s
     fn = "moe_unpermute_backward"
     d = _choice(fn, "dtype", DTYPES, dtype)
     _sizes(fn, T, H, k)
-    z, at = _ELEM[dtype], _device()
+    z = _ELEM[dtype]
+    at, st = _here(stream)
     S = T * k
     _check(lib().moe_unpermute_backward(
         _buf(fn, "dout", dout, T * H * z, dtype, at), _buf(fn, "rows", rows, S * H * z, dtype, at), d, T, H, k,
         _buf(fn, "inv", inv, 4 * S, "i32", at), _buf(fn, "topk_w", topk_w, 4 * S, "f32", at),
         _buf(fn, "drows", drows, S * H * z, dtype, at), _buf(fn, "dw", dw, 4 * S, "f32", at),
-        _stream(stream)), fn)
+        st), fn)
 
 
 def mxfp4_scale_shape(R, K, layout):
@@ -517,12 +524,13 @@ def moe_quantize_mxfp4(x, dtype, T, K, k, inv, codes, scales, scale_layout="row"
     d = _choice(fn, "dtype", DTYPES, dtype)
     s = _choice(fn, "scale_layout", SCALE_LAYOUTS, scale_layout)
     _sizes(fn, T, K, k)
-    z, at = _ELEM[dtype], _device()
+    z = _ELEM[dtype]
+    at, st = _here(stream)
     R = T * k
     _check(lib().moe_quantize_mxfp4(
         _buf(fn, "x", x, T * K * z, dtype, at), d, T, K, k, _buf(fn, "inv", inv, 4 * R, "i32", at),
         _buf(fn, "codes", codes, R * (K // 2), "u8", at),
-        _buf(fn, "scales", scales, _scale_bytes(R, K, s), "u8", at), s, _stream(stream)), fn)
+        _buf(fn, "scales", scales, _scale_bytes(R, K, s), "u8", at), s, st), fn)
 
 
 def moe_dequantize_mxfp4(codes, scales, scale_layout, R, K, dtype, out, stream=None):
@@ -531,11 +539,12 @@ def moe_dequantize_mxfp4(codes, scales, scale_layout, R, K, dtype, out, stream=N
     d = _choice(fn, "dtype", DTYPES, dtype)
     s = _choice(fn, "scale_layout", SCALE_LAYOUTS, scale_layout)
     _sizes(fn, R, K)
-    z, at = _ELEM[dtype], _device()
+    z = _ELEM[dtype]
+    at, st = _here(stream)
     _check(lib().moe_dequantize_mxfp4(
         _buf(fn, "codes", codes, R * (K // 2), "u8", at),
         _buf(fn, "scales", scales, _scale_bytes(R, K, s), "u8", at), s, R, K, d,
-        _buf(fn, "out", out, R * K * z, dtype, at), _stream(stream)), fn)
+        _buf(fn, "out", out, R * K * z, dtype, at), st), fn)
 
 
 def _weight_tiles(E, N, K):
@@ -558,11 +567,12 @@ def moe_mxfp4_prepack(w, w_scales, E, N, K, w_tiled, w_scales_chunked, stream=No
     """Weights u8 [E, N, K/2] and scales u8 [E, N, K/32] -> the layout moe_mxfp4_gemm reads."""
     fn = "moe_mxfp4_prepack"
     _sizes(fn, E, N, K)
-    tiles, at = _weight_tiles(E, N, K), _device()
+    tiles = _weight_tiles(E, N, K)
+    at, st = _here(stream)
     _check(lib().moe_mxfp4_prepack(
         _buf(fn, "w", w, E * N * (K // 2), "u8", at), _buf(fn, "w_scales", w_scales, E * N * (K // 32), "u8", at),
         E, N, K, _buf(fn, "w_tiled", w_tiled, tiles * 16384, "u8", at),
-        _buf(fn, "w_scales_chunked", w_scales_chunked, tiles * 1024, "u8", at), _stream(stream)), fn)
+        _buf(fn, "w_scales_chunked", w_scales_chunked, tiles * 1024, "u8", at), st), fn)
 
 
 def moe_mxfp4_workspace_bytes(R, E, N, K):
@@ -579,7 +589,8 @@ def moe_mxfp4_gemm(codes, scales, offsets, R, E, N, K, w_tiled, w_scales_chunked
     fn = "moe_mxfp4_gemm"
     d = _choice(fn, "dtype", DTYPES, dtype)
     _sizes(fn, R, E, N, K)
-    z, at = _ELEM[dtype], _device()
+    z = _ELEM[dtype]
+    at, st = _here(stream)
     tiles = _weight_tiles(E, N, K)
     # (Only products on CTA pairs need more than the error word's 256 bytes, and
     # they have at least 224 rows per group: small calls skip the question.)
@@ -590,9 +601,9 @@ def moe_mxfp4_gemm(codes, scales, offsets, R, E, N, K, w_tiled, w_scales_chunked
         _buf(fn, "offsets", offsets, 4 * (E + 1), "i32", at), R, E, N, K,
         _buf(fn, "w_tiled", w_tiled, tiles * 16384, "u8", at),
         _buf(fn, "w_scales_chunked", w_scales_chunked, tiles * 1024, "u8", at), d,
-        _buf(fn, "out", out, R * N * z, dtype, at), 
+        _buf(fn, "out", out, R * N * z, dtype, at),
         _buf(fn, "workspace", workspace, need, "any", at),
-        _stream(stream)), fn)
+        st), fn)
 
 
 def moe_mxfp4_clear_error(workspace, stream=None):
