@@ -531,3 +531,64 @@ def test_product_offsets_past_32_bits(R, E, N, K):
         a = O.dequantize_mxfp4(codes[r:r + 1].cpu().numpy(), np.full((1, K // 32), 127, np.uint8))
         b = O.dequantize_mxfp4(w[e].cpu().numpy(), np.full((N, K // 32), 127, np.uint8))
         assert torch.equal(out[r].cpu(), torch.from_numpy((a @ b.T)[0]).bfloat16()), r
+
+
+@pytest.mark.parametrize("counts,other,N,K", [([40, 0, 9, 15] * 4, [1, 100, 0, 3] * 4, 264, 288),
+                                              ([3000, 1000], [17, 3983], 5128, 64)], ids=["single", "pairs"])
+def test_replay_on_other_groups(counts, other, N, K):
+    """A captured product replayed on other row offsets (and other rows): the launch
+    is sized by R and E alone."""
+    ensure_built()
+    E, R = len(counts), max(sum(counts), sum(other))
+    a, sa, w, sw = _operands(R, E, N, K, 9, whole=True)
+    p = Product(R, E, N, K, a, sa, w, sw)
+    off = _cuda(_offsets(counts))
+    out = torch.full((R, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    p(off, "bf16", out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        p(off, "bf16", out)
+    for c in (other, counts, other):
+        off.copy_(_cuda(_offsets(c)))
+        p.codes.copy_(torch.roll(p.codes, 1, 0))
+        out.fill_(7.0)
+        graph.replay()
+        got = out.clone()
+        want = p(off, "bf16")
+        assert torch.equal(got, want)
+        assert (got[sum(c):] == 7.0).all() and not (got[:sum(c)] == 7.0).all()
+    p.check()
+
+
+def test_operators_on_a_plan_s_routing():
+    """The routing in a plan's workspace (moe_route, raw addresses from the view)
+    drives the operators as moe_route_static's does."""
+    ensure_built()
+    T, H, k, E, N = 96, 512, 2, 8, 136
+    g = _gen(61)
+    lay = moe.MoELayer(T, H, 256, E, k)
+    ids = torch.rand(T, E, generator=g, device="cuda").topk(k, 1).indices.to(torch.int32).contiguous()
+    ids[3, 1] = -1
+    moe.moe_route(lay.plan, ids, lay.workspace)
+    v = lay.view()
+    i32 = lambda n: torch.empty(n, dtype=torch.int32, device="cuda")  # noqa: E731
+    counts, offsets, perm, inv = i32(E), i32(E + 1), i32(T * k), i32(T * k)
+    moe.moe_route_static(ids, T, k, E, counts, offsets, perm, inv)
+    x = torch.randn(T, H, generator=g, device="cuda").to(torch.bfloat16)
+    _, _, w, sw = _operands(1, E, N, H, 4)
+    res = []
+    for iv, off in ((v.inv, v.offsets), (inv, offsets)):
+        codes = torch.zeros(T * k, H // 2, dtype=torch.uint8, device="cuda")
+        scales = torch.zeros(moe.mxfp4_scale_shape(T * k, H, "group"), dtype=torch.uint8, device="cuda")
+        moe.moe_quantize_mxfp4(x, "bf16", T, H, k, iv, codes, scales, "group")
+        p = Product(T * k, E, N, H, np.zeros((T * k, H // 2), np.uint8),
+                    np.zeros((T * k, H // 32), np.uint8), w, sw)
+        p.codes, p.scales = codes, scales
+        out = torch.zeros(T * k, N, dtype=torch.bfloat16, device="cuda")
+        p(off, "bf16", out)
+        rows = torch.zeros(T * k, H, dtype=torch.bfloat16, device="cuda")
+        moe.moe_permute(x, T, H * 2, k, iv, rows)
+        res.append((codes, scales, out, rows))
+    assert all(torch.equal(a, b) for a, b in zip(*res))
+    assert lay.check() == 0
