@@ -10,7 +10,11 @@
 //   prepack:    weights into the tiles and scale chunks the MXFP4 product reads.
 // The division by 2^n is exact, so the codes depend on the inputs alone.
 // HBM-bound: quantise reads an element once and writes 17/32 byte for it, once
-// per slot when it also copies the rows into expert order.
+// per slot when it also copies the rows into expert order (8192 x 7168 bf16: in
+// order 27 us, 5.5 TB/s; to 8 slots each 68 us, 5.4 TB/s, group-major scales, of
+// which each row's words lie apart, costing 5 of them); dequantise 65536 x 7168
+// to bf16 177 us, 6.7 TB/s.  32-byte loads and stores: with 16 bytes a thread's two
+// accesses each touch half of their sectors.
 #include <cuda_runtime.h>
 
 #include "elem.cuh"

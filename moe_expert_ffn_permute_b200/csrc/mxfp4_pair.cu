@@ -10,6 +10,10 @@
 // token tile and K block (1/16 of the codes' bytes); both SMs of a pair read the
 // whole record, since each applies the scales of all the tile's tokens.
 //
+// 65536 rows, 7168 -> 4096, 32 experts: 705 us (5.5 PFLOP/s) for a first call, 814
+// under the 1 kW cap at 1.35 GHz, where every byte moved costs clocks: without the
+// MMAs 505 us, without the output's stores 765, without the token loads 700.
+//
 // Tiles, warps and the epilogue are those of mxfp4_gemm.cu; the MMA warp of the
 // leader (rank 0) issues for both SMs.  No TMA load uses cluster multicast.
 #include <cuda.h>
