@@ -289,8 +289,8 @@ moe_status moe_quantize_act(const void *x_bf16, int T, int H, uint8_t *x_codes,
  * results repeat bitwise.  An output may overlap neither an input nor another
  * output (MOE_ERR_INVALID_ARG; the MXFP4 calls too).  All calls are one launch on `stream`, can be captured
  * into a graph, and may run concurrently with one another.
- * T >= 1, k >= 1 (k may exceed the layer's 256 experts), T*k < 2^31; rows of a
- * multiple of 16 bytes (MOE_ERR_UNSUPPORTED otherwise).                      */
+ * T >= 1, k >= 1 (k may exceed the layer's 256 experts, up to 2^24), T*k < 2^31;
+ * rows of a multiple of 16 bytes (MOE_ERR_UNSUPPORTED otherwise).            */
 typedef enum { MOE_T_BF16 = 0, MOE_T_FP16 = 1, MOE_T_FP32 = 2 } moe_dtype;
 
 /* rows[inv[t*k + j]] = x[t] for every routed slot; a copy of bytes, so any

@@ -35,11 +35,15 @@ cudaError_t ensure_max_dynamic_smem(const void* kernel, int bytes) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  std::lock_guard<std::mutex> lock(g_device_mu);
-  for (const auto& kd : g_smem_set)
-    if (kd.first == kernel && kd.second == dev) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) g_smem_set.emplace_back(kernel, dev);
+  try {   // (nothing is thrown across the ABI)
+    std::lock_guard<std::mutex> lock(g_device_mu);
+    for (const auto& kd : g_smem_set)
+      if (kd.first == kernel && kd.second == dev) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) g_smem_set.emplace_back(kernel, dev);
+  } catch (...) {
+    return cudaErrorMemoryAllocation;
+  }
   return e;
 }
 

@@ -62,6 +62,10 @@ inline bool elem_ok(int dtype) {
   return dtype == MOE_T_BF16 || dtype == MOE_T_FP16 || dtype == MOE_T_FP32;
 }
 
+// Most slots of a token the row operators and the quantiser take: their loops
+// step past k by up to a group of slots.
+constexpr int kMaxSlotsPerToken = 1 << 24;
+
 // A buffer of a call.  The operators read through the read-only path and in no
 // set order, so an output may lie neither in an input nor in another output.
 struct Buffer {

@@ -385,7 +385,7 @@ moe_status moe_quantize_mxfp4(const void* x, int dtype, int T, int K, int k, con
   if (T < 1 || K < 1 || k < 1 || static_cast<long long>(T) * k >= (1ll << 31))
     return MOE_ERR_INVALID_ARG;
   if (inv == nullptr && k != 1) return MOE_ERR_INVALID_ARG;
-  if (K % 32 != 0 || K > moe::kMaxRow) return MOE_ERR_UNSUPPORTED;
+  if (K % 32 != 0 || K > moe::kMaxRow || k > moe::kMaxSlotsPerToken) return MOE_ERR_UNSUPPORTED;
   if (!moe::aligned_to(x, 32) || !moe::aligned_to(codes, 16) || !moe::aligned_to(scales, 4) ||
       !moe::aligned_to(inv, 4))
     return MOE_ERR_ALIGNMENT;

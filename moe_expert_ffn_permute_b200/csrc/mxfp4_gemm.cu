@@ -137,6 +137,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   // MMAs alone (elect_one() says what that saves).
   if (warp == 0) {
     // ------------------------------------------------------------- operands
+    // Codes and weights that a kernel before this one wrote (generic proxy) are
+    // read by the copy engine (async proxy).
+    fence_proxy_async_global();
     const uint64_t pol_tok = l2_policy_evict_last();
     const uint64_t pol_once = l2_policy_evict_first();
     const uint64_t pol_reused = l2_policy_evict_normal();

@@ -148,6 +148,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------- operands
+    // Codes, records and weights that a kernel before this one wrote (generic
+    // proxy) are read by the copy engine (async proxy).
+    fence_proxy_async_global();
     const uint64_t pol_tok = l2_policy_evict_last();
     const uint64_t pol_w = l2_policy_evict_normal();
     const uint32_t lead_full0 = mapa_shared(smem_u32(&sm.full[0]), 0);

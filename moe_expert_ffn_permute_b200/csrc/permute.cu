@@ -210,6 +210,7 @@ moe_status check_rows(int dtype, int T, int H, int k) {
   if (!elem_ok(dtype) || T < 1 || H < 1 || k < 1) return MOE_ERR_INVALID_ARG;
   if (static_cast<long long>(T) * k >= (1ll << 31)) return MOE_ERR_INVALID_ARG;
   const long long row_bytes = static_cast<long long>(H) * elem_bytes(dtype);
+  if (k > kMaxSlotsPerToken) return MOE_ERR_UNSUPPORTED;
   if (row_bytes % 16 != 0 || copy_blocks(T, row_bytes / 16, k) == 0) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
@@ -286,7 +287,7 @@ moe_status moe_permute(const void* x, int T, int64_t row_bytes, int k, const int
   if (x == nullptr || inv == nullptr || rows == nullptr) return MOE_ERR_INVALID_ARG;
   if (T < 1 || row_bytes < 1 || k < 1 || static_cast<long long>(T) * k >= (1ll << 31))
     return MOE_ERR_INVALID_ARG;
-  if (row_bytes % 4 != 0) return MOE_ERR_UNSUPPORTED;
+  if (row_bytes % 4 != 0 || k > moe::kMaxSlotsPerToken) return MOE_ERR_UNSUPPORTED;
   if (!moe::aligned_to(x, 16) || !moe::aligned_to(rows, 16) || !moe::aligned_to(inv, 4))
     return MOE_ERR_ALIGNMENT;
   auto st = reinterpret_cast<cudaStream_t>(stream);

@@ -67,6 +67,8 @@ CASES = [
     ("moe_unpermute_backward", ALIGNMENT, dict(dw=F_ + 2)),
     ("moe_unpermute_backward", UNSUPPORTED, dict(H=20)),
     ("moe_permute", INVALID, dict(rows=B)), ("moe_permute", UNSUPPORTED, dict(T=1, k=(1 << 31) - 1, row_bytes=1 << 40)),
+    ("moe_permute", UNSUPPORTED, dict(T=1, k=(1 << 24) + 1)), ("moe_unpermute", UNSUPPORTED, dict(T=1, k=(1 << 24) + 1)),
+    ("moe_unpermute_backward", UNSUPPORTED, dict(T=1, k=1 << 30)), ("moe_quantize_mxfp4", UNSUPPORTED, dict(T=1, k=1 << 30)),
     ("moe_unpermute", INVALID, dict(out=C)), ("moe_unpermute", INVALID, dict(out=B + 16)),
     ("moe_unpermute_backward", INVALID, dict(dw=D)), ("moe_unpermute_backward", INVALID, dict(dw=C)),
     ("moe_unpermute_backward", INVALID, dict(drows=C)),
