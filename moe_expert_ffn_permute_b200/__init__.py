@@ -22,7 +22,6 @@ STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED",
                 6: "MOE_ERR_BAD_ROUTING"}
 W_DTYPES = {"e4m3": 0, "e2m1": 1, "bf16": 2}
 ACT_KINDS = {"swiglu": 0, "swiglu_oai": 1}
-DTYPES = {"bf16": 0, "fp16": 1, "fp32": 2}            # moe_dtype
 SCALE_LAYOUTS = {"row": 0, "group": 1}                # moe_scale_layout
 
 
@@ -128,30 +127,33 @@ def _ptr(v):
     raise TypeError(f"expected an address or a tensor, got {type(v)}")
 
 
+# What torch knows, looked up on the first call that needs it (_find_cuda).
 _current_device = None   # torch.cuda.current_device once CUDA is known to be there
 _raw_stream = None       # device index -> handle of its current stream
-_TYPE = {}               # names of _buf's types -> torch dtypes
+_i32 = _f32 = _u8 = None                                                    # torch dtypes
+_ELEM = {"bf16": (0, 2, None), "fp16": (1, 2, None), "fp32": (2, 4, None)}  # moe_dtype, bytes, torch's
 
 
 def _find_cuda():
     """Looks CUDA up in torch, once; False without it (the next call looks again)."""
-    global _current_device, _raw_stream
+    global _current_device, _raw_stream, _i32, _f32, _u8
     if _current_device is not None:
         return True
     try:
         import torch
     except ImportError:  # pragma: no cover
         return False
-    _TYPE.update(i32=torch.int32, f32=torch.float32, u8=torch.uint8, bf16=torch.bfloat16,
-                 fp16=torch.float16, fp32=torch.float32, any=None)
+    _i32, _f32, _u8 = torch.int32, torch.float32, torch.uint8
+    _ELEM.update(bf16=(0, 2, torch.bfloat16), fp16=(1, 2, torch.float16), fp32=(2, 4, torch.float32))
     if not torch.cuda.is_available():
         return False
-    # The current stream's handle without a Stream object around it (0.2 us a
-    # call against 3 us for current_stream().cuda_stream).
+    torch.cuda.current_device()   # initialises CUDA in torch
+    # The current device and its stream's handle without the checks and the Stream
+    # object around them (together 0.2 us a call against 3.4).
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     if _raw_stream is None:  # pragma: no cover
         _raw_stream = lambda device: torch.cuda.current_stream(device).cuda_stream  # noqa: E731
-    _current_device = torch.cuda.current_device
+    _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
     return True
 
 
@@ -410,35 +412,31 @@ def moe_forward_launch_count(plan):
     return lib().moe_forward_launch_count(plan)
 
 
+# The calls below run once per layer and token step, so their checks are written to
+# cost little: sizes in one expression, one call per buffer.
+
+
 def _sizes(fn, *values):
-    """C ints of a call: whole numbers that fit, so that none wraps around."""
-    for v in values:
-        if not -(1 << 31) <= v < (1 << 31):
-            raise MoEError(MOE_ERR_INVALID_ARG, f"{fn}: {v} does not fit a C int")
+    """Refuses a call whose sizes are negative or would wrap around as C ints."""
+    raise MoEError(MOE_ERR_INVALID_ARG, f"{fn}: sizes {values} must be C ints of at least 0")
 
 
 def _choice(fn, name, table, value):
-    try:
-        return table[value]
-    except (KeyError, TypeError):
-        raise MoEError(MOE_ERR_INVALID_ARG,
-                       f"{fn}: {name} must be one of {', '.join(table)}, got {value!r}") from None
-
-
-_ELEM = {"bf16": 2, "fp16": 2, "fp32": 4}     # bytes per element
+    """Refuses a call for an argument that is none of a table's names."""
+    raise MoEError(MOE_ERR_INVALID_ARG,
+                   f"{fn}: {name} must be one of {', '.join(table)}, got {value!r}")
 
 
 def _buf(fn, name, t, nbytes, dtype, device):
     """Address of one buffer of a call: a tensor, an address or None.  The C ABI
     sees only pointers, so a tensor is checked here: contiguous, on the current
-    CUDA device (`device`, from _here()), of type `dtype` (a key of _TYPE) and
-    at least `nbytes` long.  A raw address is passed through (the caller vouches
-    for it), and so is None (the library refuses it where it is required)."""
+    CUDA device (`device`, from _here()), of torch type `dtype` (None: any) and at
+    least `nbytes` long.  A raw address is passed through (the caller vouches for
+    it), and so is None (the library refuses it where it is required)."""
     if t is None or isinstance(t, int):
         return t
     try:
-        want = _TYPE[dtype]
-        if (t.get_device() == device and t.is_contiguous() and (want is None or t.dtype is want)
+        if (t.get_device() == device and t.is_contiguous() and (dtype is None or t.dtype is dtype)
                 and t.nbytes >= nbytes):
             return t.data_ptr()
     except AttributeError:
@@ -447,8 +445,8 @@ def _buf(fn, name, t, nbytes, dtype, device):
         what = f"must be on the current CUDA device, is on {t.device}"
     elif not t.is_contiguous():
         what = "must be contiguous"
-    elif want is not None and t.dtype is not want:
-        what = f"must be {want}, got {t.dtype}"
+    elif dtype is not None and t.dtype is not dtype:
+        what = f"must be {dtype}, got {t.dtype}"
     else:
         what = f"holds {t.nbytes} bytes, needs {nbytes}"
     raise MoEError(MOE_ERR_INVALID_ARG, f"{fn}: {name} {what}")
@@ -457,55 +455,68 @@ def _buf(fn, name, t, nbytes, dtype, device):
 def moe_permute(x, T, row_bytes, k, inv, rows, stream=None):
     """rows[inv[t, j]] = x[t]: x [T, row_bytes] of any type -> rows [T*k, row_bytes]."""
     fn = "moe_permute"
-    _sizes(fn, T, k)
-    S = T * k
+    if (T | k) >> 31:
+        _sizes(fn, T, k)
     at, st = _here(stream)
-    _check(lib().moe_permute(_buf(fn, "x", x, T * row_bytes, "any", at), T, row_bytes, k,
-                             _buf(fn, "inv", inv, 4 * S, "i32", at),
-                             _buf(fn, "rows", rows, S * row_bytes, "any", at), st), fn)
+    S = T * k
+    status = (_lib or lib()).moe_permute(
+        _buf(fn, "x", x, T * row_bytes, None, at), T, row_bytes, k,
+        _buf(fn, "inv", inv, 4 * S, _i32, at), _buf(fn, "rows", rows, S * row_bytes, None, at), st)
+    if status:
+        raise MoEError(status, fn)
 
 
 def moe_permute_backward(drows, dtype, T, H, k, inv, dx, stream=None):
     """dx[t] = sum_j drows[inv[t, j]]; dtype "bf16", "fp16" or "fp32"."""
     fn = "moe_permute_backward"
-    d = _choice(fn, "dtype", DTYPES, dtype)
-    _sizes(fn, T, H, k)
-    z = _ELEM[dtype]
+    if dtype not in _ELEM:
+        _choice(fn, "dtype", _ELEM, dtype)
+    if (T | H | k) >> 31:
+        _sizes(fn, T, H, k)
     at, st = _here(stream)
+    d, z, tt = _ELEM[dtype]
     S = T * k
-    _check(lib().moe_permute_backward(_buf(fn, "drows", drows, S * H * z, dtype, at), d, T, H, k,
-                                      _buf(fn, "inv", inv, 4 * S, "i32", at),
-                                      _buf(fn, "dx", dx, T * H * z, dtype, at), st), fn)
+    status = (_lib or lib()).moe_permute_backward(
+        _buf(fn, "drows", drows, S * H * z, tt, at), d, T, H, k, _buf(fn, "inv", inv, 4 * S, _i32, at),
+        _buf(fn, "dx", dx, T * H * z, tt, at), st)
+    if status:
+        raise MoEError(status, fn)
 
 
 def moe_unpermute(rows, dtype, T, H, k, inv, topk_w, out, stream=None):
     """out[t] = sum_j topk_w[t, j] * rows[inv[t, j]]; dtype "bf16", "fp16" or "fp32"."""
     fn = "moe_unpermute"
-    d = _choice(fn, "dtype", DTYPES, dtype)
-    _sizes(fn, T, H, k)
-    z = _ELEM[dtype]
+    if dtype not in _ELEM:
+        _choice(fn, "dtype", _ELEM, dtype)
+    if (T | H | k) >> 31:
+        _sizes(fn, T, H, k)
     at, st = _here(stream)
+    d, z, tt = _ELEM[dtype]
     S = T * k
-    _check(lib().moe_unpermute(_buf(fn, "rows", rows, S * H * z, dtype, at), d, T, H, k,
-                               _buf(fn, "inv", inv, 4 * S, "i32", at),
-                               _buf(fn, "topk_w", topk_w, 4 * S, "f32", at),
-                               _buf(fn, "out", out, T * H * z, dtype, at), st), fn)
+    status = (_lib or lib()).moe_unpermute(
+        _buf(fn, "rows", rows, S * H * z, tt, at), d, T, H, k, _buf(fn, "inv", inv, 4 * S, _i32, at),
+        _buf(fn, "topk_w", topk_w, 4 * S, _f32, at), _buf(fn, "out", out, T * H * z, tt, at), st)
+    if status:
+        raise MoEError(status, fn)
 
 
 def moe_unpermute_backward(dout, rows, dtype, T, H, k, inv, topk_w, drows, dw, stream=None):
     """drows[inv[t, j]] = topk_w[t, j] * dout[t]; dw[t, j] = <dout[t], rows[inv[t, j]]>.
     drows or dw may be None; rows too when dw is."""
     fn = "moe_unpermute_backward"
-    d = _choice(fn, "dtype", DTYPES, dtype)
-    _sizes(fn, T, H, k)
-    z = _ELEM[dtype]
+    if dtype not in _ELEM:
+        _choice(fn, "dtype", _ELEM, dtype)
+    if (T | H | k) >> 31:
+        _sizes(fn, T, H, k)
     at, st = _here(stream)
+    d, z, tt = _ELEM[dtype]
     S = T * k
-    _check(lib().moe_unpermute_backward(
-        _buf(fn, "dout", dout, T * H * z, dtype, at), _buf(fn, "rows", rows, S * H * z, dtype, at), d, T, H, k,
-        _buf(fn, "inv", inv, 4 * S, "i32", at), _buf(fn, "topk_w", topk_w, 4 * S, "f32", at),
-        _buf(fn, "drows", drows, S * H * z, dtype, at), _buf(fn, "dw", dw, 4 * S, "f32", at),
-        st), fn)
+    status = (_lib or lib()).moe_unpermute_backward(
+        _buf(fn, "dout", dout, T * H * z, tt, at), _buf(fn, "rows", rows, S * H * z, tt, at), d, T, H,
+        k, _buf(fn, "inv", inv, 4 * S, _i32, at), _buf(fn, "topk_w", topk_w, 4 * S, _f32, at),
+        _buf(fn, "drows", drows, S * H * z, tt, at), _buf(fn, "dw", dw, 4 * S, _f32, at), st)
+    if status:
+        raise MoEError(status, fn)
 
 
 def mxfp4_scale_shape(R, K, layout):
@@ -521,30 +532,51 @@ def moe_quantize_mxfp4(x, dtype, T, K, k, inv, codes, scales, scale_layout="row"
     """x [T, K] -> E2M1 codes u8 [T*k, K/2] and UE8M0 scales (mxfp4_scale_shape), each
     token's row at the positions of its slots; inv None (k = 1): in order."""
     fn = "moe_quantize_mxfp4"
-    d = _choice(fn, "dtype", DTYPES, dtype)
-    s = _choice(fn, "scale_layout", SCALE_LAYOUTS, scale_layout)
-    _sizes(fn, T, K, k)
-    z = _ELEM[dtype]
+    if dtype not in _ELEM:
+        _choice(fn, "dtype", _ELEM, dtype)
+    if scale_layout not in SCALE_LAYOUTS:
+        _choice(fn, "scale_layout", SCALE_LAYOUTS, scale_layout)
+    if (T | K | k) >> 31:
+        _sizes(fn, T, K, k)
     at, st = _here(stream)
+    d, z, tt = _ELEM[dtype]
+    s = SCALE_LAYOUTS[scale_layout]
     R = T * k
-    _check(lib().moe_quantize_mxfp4(
-        _buf(fn, "x", x, T * K * z, dtype, at), d, T, K, k, _buf(fn, "inv", inv, 4 * R, "i32", at),
-        _buf(fn, "codes", codes, R * (K // 2), "u8", at),
-        _buf(fn, "scales", scales, _scale_bytes(R, K, s), "u8", at), s, st), fn)
+    status = (_lib or lib()).moe_quantize_mxfp4(
+        _buf(fn, "x", x, T * K * z, tt, at), d, T, K, k, _buf(fn, "inv", inv, 4 * R, _i32, at),
+        _buf(fn, "codes", codes, R * (K // 2), _u8, at),
+        _buf(fn, "scales", scales, _scale_bytes(R, K, s), _u8, at), s, st)
+    if status:
+        raise MoEError(status, fn)
 
 
 def moe_dequantize_mxfp4(codes, scales, scale_layout, R, K, dtype, out, stream=None):
     """The values of codes u8 [R, K/2] and their scales -> out [R, K]."""
     fn = "moe_dequantize_mxfp4"
-    d = _choice(fn, "dtype", DTYPES, dtype)
-    s = _choice(fn, "scale_layout", SCALE_LAYOUTS, scale_layout)
-    _sizes(fn, R, K)
-    z = _ELEM[dtype]
+    if dtype not in _ELEM:
+        _choice(fn, "dtype", _ELEM, dtype)
+    if scale_layout not in SCALE_LAYOUTS:
+        _choice(fn, "scale_layout", SCALE_LAYOUTS, scale_layout)
+    if (R | K) >> 31:
+        _sizes(fn, R, K)
     at, st = _here(stream)
-    _check(lib().moe_dequantize_mxfp4(
-        _buf(fn, "codes", codes, R * (K // 2), "u8", at),
-        _buf(fn, "scales", scales, _scale_bytes(R, K, s), "u8", at), s, R, K, d,
-        _buf(fn, "out", out, R * K * z, dtype, at), st), fn)
+    d, z, tt = _ELEM[dtype]
+    s = SCALE_LAYOUTS[scale_layout]
+    status = (_lib or lib()).moe_dequantize_mxfp4(
+        _buf(fn, "codes", codes, R * (K // 2), _u8, at),
+        _buf(fn, "scales", scales, _scale_bytes(R, K, s), _u8, at), s, R, K, d,
+        _buf(fn, "out", out, R * K * z, tt, at), st)
+    if status:
+        raise MoEError(status, fn)
+
+
+def moe_mxfp4_weight_bytes(E, N, K):
+    """Bytes of prepacked weights (0: sizes moe_mxfp4_gemm does not take)."""
+    return 0 if (E | N | K) >> 31 else lib().moe_mxfp4_weight_bytes(E, N, K)
+
+
+def moe_mxfp4_weight_scale_bytes(E, N, K):
+    return 0 if (E | N | K) >> 31 else lib().moe_mxfp4_weight_scale_bytes(E, N, K)
 
 
 def _weight_tiles(E, N, K):
@@ -552,33 +584,23 @@ def _weight_tiles(E, N, K):
     return E * -(-N // 128) * -(-K // 256)
 
 
-def moe_mxfp4_weight_bytes(E, N, K):
-    """Bytes of prepacked weights (0: sizes moe_mxfp4_gemm does not take)."""
-    _sizes("moe_mxfp4_weight_bytes", E, N, K)
-    return lib().moe_mxfp4_weight_bytes(E, N, K)
-
-
-def moe_mxfp4_weight_scale_bytes(E, N, K):
-    _sizes("moe_mxfp4_weight_scale_bytes", E, N, K)
-    return lib().moe_mxfp4_weight_scale_bytes(E, N, K)
-
-
 def moe_mxfp4_prepack(w, w_scales, E, N, K, w_tiled, w_scales_chunked, stream=None):
     """Weights u8 [E, N, K/2] and scales u8 [E, N, K/32] -> the layout moe_mxfp4_gemm reads."""
     fn = "moe_mxfp4_prepack"
-    _sizes(fn, E, N, K)
-    tiles = _weight_tiles(E, N, K)
+    if (E | N | K) >> 31:
+        _sizes(fn, E, N, K)
     at, st = _here(stream)
+    tiles = _weight_tiles(E, N, K)
     _check(lib().moe_mxfp4_prepack(
-        _buf(fn, "w", w, E * N * (K // 2), "u8", at), _buf(fn, "w_scales", w_scales, E * N * (K // 32), "u8", at),
-        E, N, K, _buf(fn, "w_tiled", w_tiled, tiles * 16384, "u8", at),
-        _buf(fn, "w_scales_chunked", w_scales_chunked, tiles * 1024, "u8", at), st), fn)
+        _buf(fn, "w", w, E * N * (K // 2), _u8, at),
+        _buf(fn, "w_scales", w_scales, E * N * (K // 32), _u8, at), E, N, K,
+        _buf(fn, "w_tiled", w_tiled, tiles * 16384, _u8, at),
+        _buf(fn, "w_scales_chunked", w_scales_chunked, tiles * 1024, _u8, at), st), fn)
 
 
 def moe_mxfp4_workspace_bytes(R, E, N, K):
     """Bytes of moe_mxfp4_gemm's workspace on the current device (0: sizes it does not take)."""
-    _sizes("moe_mxfp4_workspace_bytes", R, E, N, K)
-    return lib().moe_mxfp4_workspace_bytes(R, E, N, K)
+    return 0 if (R | E | N | K) >> 31 else lib().moe_mxfp4_workspace_bytes(R, E, N, K)
 
 
 def moe_mxfp4_gemm(codes, scales, offsets, R, E, N, K, w_tiled, w_scales_chunked, dtype, out,
@@ -587,23 +609,25 @@ def moe_mxfp4_gemm(codes, scales, offsets, R, E, N, K, w_tiled, w_scales_chunked
     group): codes u8 [R, K/2] with group-major scales, prepacked weights, out [R, N]
     "bf16" or "fp16".  workspace: moe_mxfp4_workspace_bytes, zeroed before its first use."""
     fn = "moe_mxfp4_gemm"
-    d = _choice(fn, "dtype", DTYPES, dtype)
-    _sizes(fn, R, E, N, K)
-    z = _ELEM[dtype]
+    if dtype not in _ELEM:
+        _choice(fn, "dtype", _ELEM, dtype)
+    if (R | E | N | K) >> 31:
+        _sizes(fn, R, E, N, K)
     at, st = _here(stream)
+    d, z, tt = _ELEM[dtype]
     tiles = _weight_tiles(E, N, K)
     # (Only products on CTA pairs need more than the error word's 256 bytes, and
     # they have at least 224 rows per group: small calls skip the question.)
     need = 256 if R < 224 * E else lib().moe_mxfp4_workspace_bytes(R, E, N, K)
-    _check(lib().moe_mxfp4_gemm(
-        _buf(fn, "codes", codes, R * (K // 2), "u8", at),
-        _buf(fn, "scales", scales, _scale_bytes(R, K, 1), "u8", at),
-        _buf(fn, "offsets", offsets, 4 * (E + 1), "i32", at), R, E, N, K,
-        _buf(fn, "w_tiled", w_tiled, tiles * 16384, "u8", at),
-        _buf(fn, "w_scales_chunked", w_scales_chunked, tiles * 1024, "u8", at), d,
-        _buf(fn, "out", out, R * N * z, dtype, at),
-        _buf(fn, "workspace", workspace, need, "any", at),
-        st), fn)
+    status = (_lib or lib()).moe_mxfp4_gemm(
+        _buf(fn, "codes", codes, R * (K // 2), _u8, at),
+        _buf(fn, "scales", scales, (K + 127) // 128 * R * 4, _u8, at),
+        _buf(fn, "offsets", offsets, 4 * (E + 1), _i32, at), R, E, N, K,
+        _buf(fn, "w_tiled", w_tiled, tiles * 16384, _u8, at),
+        _buf(fn, "w_scales_chunked", w_scales_chunked, tiles * 1024, _u8, at), d,
+        _buf(fn, "out", out, R * N * z, tt, at), _buf(fn, "workspace", workspace, need, None, at), st)
+    if status:
+        raise MoEError(status, fn)
 
 
 def moe_mxfp4_clear_error(workspace, stream=None):
