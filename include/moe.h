@@ -282,15 +282,17 @@ moe_status moe_quantize_act(const void *x_bf16, int T, int H, uint8_t *x_codes,
  * They take the routing that moe_route() or moe_route_static() computes: inv
  * i32[T*k], the position of slot t*k + j in expert order, each position used
  * once, -1 for a slot that is not routed.  A position outside [0, T*k) is
- * treated as -1.  (If two slots name one position, the row written there is one
- * of the two.)  Rows are S = T*k rows of H elements in expert order; rows that no slot names --
- * behind the last routed one -- are neither read nor written.  Sums run in
- * fp32, j ascending, and are rounded once to the row type; no atomics, so
- * results repeat bitwise.  An output may overlap neither an input nor another
- * output (MOE_ERR_INVALID_ARG; the MXFP4 calls too).  All calls are one launch on `stream`, can be captured
- * into a graph, and may run concurrently with one another.
- * T >= 1, k >= 1 (k may exceed the layer's 256 experts, up to 2^24), T*k < 2^31;
- * rows of a multiple of 16 bytes (MOE_ERR_UNSUPPORTED otherwise).            */
+ * treated as -1.  (If two slots name one position, the row written there may
+ * mix theirs.)  Rows are S = T*k rows of H elements in expert order; rows that
+ * no slot names -- behind the last routed one -- are neither read nor written.
+ * Sums run in fp32, j ascending, and are rounded once to the row type; no
+ * atomics, so results repeat bitwise.  An output may overlap neither an input
+ * nor another output (MOE_ERR_INVALID_ARG; the MXFP4 calls too).  Every call is
+ * one launch on `stream`, can be captured into a graph, and may run
+ * concurrently with others.  T >= 1, k >= 1 (it may exceed the layer's 256
+ * experts, up to 2^24), T*k < 2^31; rows of a multiple of 16 bytes
+ * (MOE_ERR_UNSUPPORTED otherwise); tensors 16-byte, inv, topk_w and dw 4-byte
+ * aligned.                                                                  */
 typedef enum { MOE_T_BF16 = 0, MOE_T_FP16 = 1, MOE_T_FP32 = 2 } moe_dtype;
 
 /* rows[inv[t*k + j]] = x[t] for every routed slot; a copy of bytes, so any
@@ -372,8 +374,8 @@ size_t moe_mxfp4_weight_scale_bytes(int E, int N, int K);
 /* Lay out MXFP4 weights for moe_mxfp4_gemm, once per weight set: w u8 [E, N,
  * K/2] and w_scales u8 [E, N, K/32] row-major -> tiles of 128 rows x 256 codes,
  * 16 KB each, swizzled as the tensor core reads them, and the scale chunks that
- * go with them (N and K are filled up with zeros to whole tiles).  Buffers
- * 16-byte aligned, not overlapping.  Enqueued on `stream`.
+ * go with them (N and K are filled up with zeros to whole tiles).  w and the
+ * outputs 16-byte aligned.  Enqueued on `stream`.
  * No counterpart on the pages (a storage layout for this library's tensor-
  * core kernels).
  */
@@ -382,8 +384,8 @@ moe_status moe_mxfp4_prepack(const uint8_t *w, const uint8_t *w_scales, int E, i
 
 /* Bytes of moe_mxfp4_gemm's workspace (device, 256-byte aligned); 0 for sizes it
  * does not take; for the current device.  Zero the workspace once before its
- * first use; calls leave it ready for the next (of the same or other sizes that
- * it is large enough for).  Calls that may overlap on the GPU need workspaces of
+ * first use (or moe_mxfp4_clear_error it); calls leave it ready for the next, of
+ * the same or other sizes that it is large enough for.  Calls that may overlap on the GPU need workspaces of
  * their own.
  * No counterpart on the pages.
  */

@@ -127,6 +127,13 @@ def test_other_objects_are_a_type_error():
         moe.moe_permute(np.zeros(4), 1, 16, 1, B, C, stream=0)
 
 
+def test_default_stream_without_a_gpu():
+    """No stream given: the refusal is the library's, with or without CUDA in torch."""
+    with pytest.raises(moe.MoEError) as e:
+        moe.moe_permute(A, 4, 255, 2, B, C)
+    assert e.value.status == UNSUPPORTED
+
+
 def test_sizes_that_do_not_fit_are_refused():
     _refused(INVALID, "moe_unpermute", T=(1 << 32) + 4)
     _refused(INVALID, "moe_mxfp4_gemm", K=(1 << 32) + 64)
