@@ -133,60 +133,57 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int my_tiles = uniform(
       static_cast<int>((tiles - blockIdx.x + gridDim.x - 1) / gridDim.x));   // may be <= 0
 
-  // The issuing warps run warp-uniform loops and elect a lane for the copies and
-  // MMAs alone (elect_one() says what that saves).
+  // The issuing loops run on one elected lane (elect_one() says why not on lane 0).
   if (warp == 0) {
     // ------------------------------------------------------------- operands
-    // Codes and weights that a kernel before this one wrote (generic proxy) are
-    // read by the copy engine (async proxy).
-    fence_proxy_async_global();
-    const uint64_t pol_tok = l2_policy_evict_last();
-    const uint64_t pol_once = l2_policy_evict_first();
-    const uint64_t pol_reused = l2_policy_evict_normal();
-    int stage = 0;
-    uint32_t phase = 0;
-    long long issued = 0;   // stages filled
-    bool ok = true;
-    for (int i = 0; ok && i < my_tiles; ++i) {
-      const Tile t =
-          tile_at(sm.groups, p.E, p.nb_n, blockIdx.x + static_cast<long long>(i) * gridDim.x);
-      // Weights of an expert with one token tile are read once.
-      const uint64_t pol_w =
-          sm.groups.tile_off[t.e + 1] - sm.groups.tile_off[t.e] > 1 ? pol_reused : pol_once;
-      const int boxes = uniform((t.rows + C::kBox - 1) / C::kBox);
-      const uint32_t bytes = kTileBytes + 1024 + boxes * C::kBox * kKBytes;
-      const long long block = uniform((static_cast<long long>(t.e) * p.nb_n + t.nb) * kb_n);
-      const int row = uniform(t.row);
-      for (int kb = 0; kb < kb_n; ++kb) {
-        if (!mbar_wait_warp(&sm.empty[stage], phase ^ 1u, p.err, &sm.abort_flag)) {
-          ok = false;
-          break;
-        }
-        if (elect_one()) {
+    if (elect_one()) {
+      // Codes and weights that a kernel before this one wrote (generic proxy) are
+      // read by the copy engine (async proxy).
+      fence_proxy_async_global();
+      const uint64_t pol_tok = l2_policy_evict_last();
+      const uint64_t pol_once = l2_policy_evict_first();
+      const uint64_t pol_reused = l2_policy_evict_normal();
+      int stage = 0;
+      uint32_t phase = 0;
+      long long issued = 0;   // stages filled
+      bool ok = true;
+      for (int i = 0; ok && i < my_tiles; ++i) {
+        const Tile t =
+            tile_at(sm.groups, p.E, p.nb_n, blockIdx.x + static_cast<long long>(i) * gridDim.x);
+        // Weights of an expert with one token tile are read once.
+        const uint64_t pol_w =
+            sm.groups.tile_off[t.e + 1] - sm.groups.tile_off[t.e] > 1 ? pol_reused : pol_once;
+        const int boxes = (t.rows + C::kBox - 1) / C::kBox;
+        const uint32_t bytes = kTileBytes + 1024 + boxes * C::kBox * kKBytes;
+        const long long block = (static_cast<long long>(t.e) * p.nb_n + t.nb) * kb_n;
+        for (int kb = 0; kb < kb_n; ++kb) {
+          if (!mbar_wait(&sm.empty[stage], phase ^ 1u, p.err, &sm.abort_flag)) {
+            ok = false;
+            break;
+          }
           mbar_arrive_expect_tx(&sm.full[stage], bytes);
           bulk_load_hint(sm.w[stage], p.w + (block + kb) * kTileBytes, kTileBytes, &sm.full[stage],
                          pol_w);
           bulk_load_hint(sm.sfw[stage], p.w_sf + (block + kb) * 1024, 1024, &sm.full[stage], pol_w);
           for (int b = 0; b < boxes; ++b)
             tma_load_2d(sm.t[stage] + b * C::kBox * kKBytes, &tmap, kb * kKBytes,
-                        row + b * C::kBox, &sm.full[stage], pol_tok);
+                        t.row + b * C::kBox, &sm.full[stage], pol_tok);
+          ++issued;
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
         }
-        __syncwarp();
-        ++issued;
-        if (++stage == STAGES) {
-          stage = 0;
+      }
+      // On the way out of an aborted CTA: its copies in flight land before its
+      // shared memory is given back.
+      for (int s = 0; !ok && s < STAGES && s < issued; ++s) {
+        if (--stage < 0) {
+          stage = STAGES - 1;
           phase ^= 1u;
         }
+        mbar_wait_limited(&sm.full[stage], phase, kWaitLimitNs);
       }
-    }
-    // On the way out of an aborted CTA: its copies in flight land before its
-    // shared memory is given back.
-    for (int s = 0; !ok && s < STAGES && s < issued; ++s) {
-      if (--stage < 0) {
-        stage = STAGES - 1;
-        phase ^= 1u;
-      }
-      mbar_wait_limited(&sm.full[stage], phase, kWaitLimitNs);
     }
     __syncwarp();
   } else if (warp == 2 || warp == 3) {
@@ -227,33 +224,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issue
-    int stage = 0;
-    uint32_t phase = 0, acc_phase = 0, set = 0;
-    const uint32_t acc = uniform(tmem);
-    const uint64_t w_desc0 = umma_desc_sw128(smem_u32(sm.w[0]));
-    const uint64_t t_desc0 = umma_desc_sw128(smem_u32(sm.t[0]));
-    const uint64_t sfw_desc0 = sf_desc(smem_u32(sm.sfw[0]));
-    const uint64_t sft_desc0 = sf_desc(smem_u32(sm.sft[0]));
-    constexpr uint64_t kKStep = 32 >> 4, kSfChunk = 512 >> 4;
-    bool ok = true;
-    for (int i = 0; ok && i < my_tiles; ++i) {
-      const Tile t =
-          tile_at(sm.groups, p.E, p.nb_n, blockIdx.x + static_cast<long long>(i) * gridDim.x);
-      const uint32_t n = uniform(mma_n(t.rows));
-      const uint32_t idesc0 = mxf4_idesc(n, 0);
-      if (!mbar_wait_warp(&sm.tmem_empty, acc_phase ^ 1u, p.err, &sm.abort_flag)) break;
-      tc_fence_after();
-      for (int kb = 0; kb < kb_n; ++kb) {
-        if (!mbar_wait_warp(&sm.full[stage], phase, p.err, &sm.abort_flag) ||
-            !mbar_wait_warp(&sm.full_sf[stage], phase, p.err, &sm.abort_flag)) {
-          ok = false;
-          break;
-        }
-        // The token scales land by cp.async (generic proxy): order them before
-        // the tensor core's (async proxy) reads.
-        fence_proxy_async_smem();
+    if (elect_one()) {
+      int stage = 0;
+      uint32_t phase = 0, acc_phase = 0, set = 0;
+      const uint32_t acc = tmem;
+      const uint64_t w_desc0 = umma_desc_sw128(smem_u32(sm.w[0]));
+      const uint64_t t_desc0 = umma_desc_sw128(smem_u32(sm.t[0]));
+      const uint64_t sfw_desc0 = sf_desc(smem_u32(sm.sfw[0]));
+      const uint64_t sft_desc0 = sf_desc(smem_u32(sm.sft[0]));
+      constexpr uint64_t kKStep = 32 >> 4, kSfChunk = 512 >> 4;
+      bool ok = true;
+      for (int i = 0; ok && i < my_tiles; ++i) {
+        const Tile t =
+            tile_at(sm.groups, p.E, p.nb_n, blockIdx.x + static_cast<long long>(i) * gridDim.x);
+        const uint32_t n = mma_n(t.rows);
+        const uint32_t idesc0 = mxf4_idesc(n, 0);
+        if (!mbar_wait(&sm.tmem_empty, acc_phase ^ 1u, p.err, &sm.abort_flag)) break;
         tc_fence_after();
-        if (elect_one()) {
+        for (int kb = 0; kb < kb_n; ++kb) {
+          if (!mbar_wait(&sm.full[stage], phase, p.err, &sm.abort_flag) ||
+              !mbar_wait(&sm.full_sf[stage], phase, p.err, &sm.abort_flag)) {
+            ok = false;
+            break;
+          }
+          // The token scales land by cp.async (generic proxy): order them before
+          // the tensor core's (async proxy) reads.
+          fence_proxy_async_smem();
+          tc_fence_after();
           const uint32_t sfw = acc + kSfCol + set * kSfSet;
           const uint32_t sft = sfw + kSfTokens;
           const uint64_t sfwd = sfw_desc0 + static_cast<uint64_t>(stage) * (1024 >> 4);
@@ -278,21 +275,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                      (sft + 8 * h) | (sf_id << 30), (kb > 0 || ks > 0) ? 1u : 0u);
           }
           tc_commit(&sm.empty[stage]);
+          set ^= 1u;
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
         }
-        __syncwarp();
-        set ^= 1u;
-        if (++stage == STAGES) {
-          stage = 0;
-          phase ^= 1u;
-        }
+        if (!ok) break;
+        tc_commit(&sm.tmem_full);
+        acc_phase ^= 1u;
       }
-      if (!ok) break;
-      if (elect_one()) tc_commit(&sm.tmem_full);
-      __syncwarp();
-      acc_phase ^= 1u;
-    }
-    // Everything issued above completes before the TMEM is freed.
-    if (elect_one()) {
+      // Everything issued above completes before the TMEM is freed.
       tc_commit(&sm.drain);
       if (!mbar_wait_limited(&sm.drain, 0, kWaitLimitNs)) atomicOr(p.err, kErrTimeoutBit);
     }
@@ -384,19 +377,23 @@ int tile_cap(int R, int E, int nb_n) {
   if (E > 1 && R <= kFewRows * E) return 128;
   const long long groups = std::min(E, R), rows = (R + groups - 1) / groups;
   const int ctas = sm_count();
-  int best = 256;
+  long long best = 256, best_size = 256;
   double least = 0;
-  for (int cap = 256; cap >= 64; cap -= 16) {
+  for (long long cap = 256; cap >= 64; cap -= 16) {
     const long long per = (rows + cap - 1) / cap, tiles = per * groups * nb_n;
     const long long size = ((rows + per - 1) / per + 15) / 16 * 16;
     const double cost =
         static_cast<double>((tiles + ctas - 1) / ctas) * (kBlockClocks + kTokenClocks * size);
-    if (cap == 256 || cost <= least) {
+    if (cap == 256 || cost < least) {
       least = cost;
       best = cap;
+      best_size = size;
     }
   }
-  return best;
+  // One group's tiles have just the size they were given; several groups get the
+  // largest cap of the same cost, so that one a little over the average is not
+  // cut in two (144 rows per group: 79 us, 94 with tiles of 144).
+  return static_cast<int>(E == 1 ? best_size : best);
 }
 
 // CTA pairs (mxfp4_pair.cu) where the average group fills most of a 256-row tile

@@ -148,58 +148,57 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------- operands
-    // Codes, records and weights that a kernel before this one wrote (generic
-    // proxy) are read by the copy engine (async proxy).
-    fence_proxy_async_global();
-    const uint64_t pol_tok = l2_policy_evict_last();
-    const uint64_t pol_w = l2_policy_evict_normal();
-    const uint32_t lead_full0 = mapa_shared(smem_u32(&sm.full[0]), 0);
-    int stage = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    for (int i = 0; ok && i < my_tiles; ++i) {
-      const Tile t = tile(i);
-      // A pair whose second block is past N reads some other block (or zeros
-      // past the last one) and stores nothing of it.
-      const long long nb = 2ll * t.nb + rank;
-      const int block = uniform(static_cast<int>((static_cast<long long>(t.e) * p.nb_n + nb) * kb_n));
-      const int row = uniform(t.row + rank * (mma_n(t.rows) / 2));
-      const int rec = uniform(static_cast<int>(
-          (cluster + static_cast<long long>(i) * clusters) / pairs_n * kb_n));
-      for (int kb = 0; kb < kb_n; ++kb) {
-        if (!mbar_wait_warp(&sm.empty[stage], phase ^ 1u, p.err, &sm.abort_flag)) {
-          ok = false;
-          break;
-        }
-        const uint32_t bar = lead_full0 + stage * 8;
-        if (elect_one()) {
+    if (elect_one()) {
+      // Codes, records and weights that a kernel before this one wrote (generic
+      // proxy) are read by the copy engine (async proxy).
+      fence_proxy_async_global();
+      const uint64_t pol_tok = l2_policy_evict_last();
+      const uint64_t pol_w = l2_policy_evict_normal();
+      const uint32_t lead_full0 = mapa_shared(smem_u32(&sm.full[0]), 0);
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int i = 0; ok && i < my_tiles; ++i) {
+        const Tile t = tile(i);
+        // A pair whose second block is past N reads some other block (or zeros
+        // past the last one) and stores nothing of it.
+        const long long nb = 2ll * t.nb + rank;
+        const int block = static_cast<int>((static_cast<long long>(t.e) * p.nb_n + nb) * kb_n);
+        const int row = t.row + rank * (mma_n(t.rows) / 2);
+        const int rec = static_cast<int>(
+            (cluster + static_cast<long long>(i) * clusters) / pairs_n * kb_n);
+        for (int kb = 0; kb < kb_n; ++kb) {
+          if (!mbar_wait(&sm.empty[stage], phase ^ 1u, p.err, &sm.abort_flag)) {
+            ok = false;
+            break;
+          }
+          const uint32_t bar = lead_full0 + stage * 8;
           if (leader) mbar_arrive_expect_tx(&sm.full[stage], kStageTx);
           tma_load_2d_pair(sm.w[stage], &tm.w, 0, (block + kb) * 128, bar, pol_w);
           tma_load_2d_pair(sm.t[stage], &tm.t, kb * kKBytes, row, bar, pol_tok);
           tma_load_2d_pair(sm.sfw[stage], &tm.sfw, 0, (block + kb) * 4, bar, pol_w);
           tma_load_2d_pair(sm.sft[stage], &tm.sft, 0, (rec + kb) * 8, bar, pol_tok);
-        }
-        __syncwarp();
-        if (++stage == kStages) {
-          stage = 0;
-          phase ^= 1u;
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
         }
       }
-    }
-    if (!ok) {
-      // On the way out of an aborted pair: the copies in flight (microseconds)
-      // land before the shared memory is given back.  Their barrier is the
-      // leader's and may never complete, so this waits by time.
-      const uint64_t t0 = globaltimer();
-      while (globaltimer() - t0 < 1000000ull) __nanosleep(1000);
+      if (!ok) {
+        // On the way out of an aborted pair: the copies in flight (microseconds)
+        // land before the shared memory is given back.  Their barrier is the
+        // leader's and may never complete, so this waits by time.
+        const uint64_t t0 = globaltimer();
+        while (globaltimer() - t0 < 1000000ull) __nanosleep(1000);
+      }
     }
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issue
-    if (leader) {
+    if (leader && elect_one()) {
       int stage = 0;
       uint32_t phase = 0, acc_phase = 0, set = 0;
-      const uint32_t acc = uniform(tmem);
+      const uint32_t acc = tmem;
       const uint64_t w_desc0 = umma_desc_sw128(smem_u32(sm.w[0]));
       const uint64_t t_desc0 = umma_desc_sw128(smem_u32(sm.t[0]));
       const uint64_t sfw_desc0 = sf_desc(smem_u32(sm.sfw[0]));
@@ -207,42 +206,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint64_t kKStep = 32 >> 4, kSfChunk = 512 >> 4;
       bool ok = true;
       for (int i = 0; ok && i < my_tiles; ++i) {
-        const uint32_t n = uniform(static_cast<uint32_t>(mma_n(tile(i).rows)));
+        const uint32_t n = static_cast<uint32_t>(mma_n(tile(i).rows));
         const uint32_t idesc0 = mxf4_idesc_m256(n, 0);
-        if (!__all_sync(0xffffffffu, mbar_wait_cluster(&sm.tmem_empty, acc_phase ^ 1u, p.err,
-                                                       &sm.abort_flag)))
-          break;
+        if (!mbar_wait_cluster(&sm.tmem_empty, acc_phase ^ 1u, p.err, &sm.abort_flag)) break;
         tc_fence_after();
         for (int kb = 0; kb < kb_n; ++kb) {
-          if (!mbar_wait_warp(&sm.full[stage], phase, p.err, &sm.abort_flag)) {
+          if (!mbar_wait(&sm.full[stage], phase, p.err, &sm.abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          if (elect_one()) {
-            const uint32_t sfw = acc + kSfCol + set * kSfSet;
-            const uint32_t sft = sfw + kSfTokens;
-            const uint64_t sfwd = sfw_desc0 + static_cast<uint64_t>(stage) * (1024 >> 4);
-            const uint64_t sftd = sft_desc0 + static_cast<uint64_t>(stage) * (kRecordBytes >> 4);
+          const uint32_t sfw = acc + kSfCol + set * kSfSet;
+          const uint32_t sft = sfw + kSfTokens;
+          const uint64_t sfwd = sfw_desc0 + static_cast<uint64_t>(stage) * (1024 >> 4);
+          const uint64_t sftd = sft_desc0 + static_cast<uint64_t>(stage) * (kRecordBytes >> 4);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              tmem_cp_pair_32x128b_warpx4(sfw + 4 * h, sfwd + h * kSfChunk);
-              tmem_cp_pair_32x128b_warpx4(sft + 8 * h, sftd + 2 * h * kSfChunk);
-              if (n > 128)
-                tmem_cp_pair_32x128b_warpx4(sft + 8 * h + 4, sftd + (2 * h + 1) * kSfChunk);
-            }
-            const uint64_t wd = w_desc0 + static_cast<uint64_t>(stage) * (kTileBytes >> 4);
-            const uint64_t td = t_desc0 + static_cast<uint64_t>(stage) * (kHalfTok * kKBytes >> 4);
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks) {
-              const uint32_t h = ks >> 1, sf_id = (ks & 1) * 2;
-              mma_mxf4_pair(acc, wd + ks * kKStep, td + ks * kKStep,
-                            idesc0 | (sf_id << 4) | (sf_id << 29), (sfw + 4 * h) | (sf_id << 30),
-                            (sft + 8 * h) | (sf_id << 30), (kb > 0 || ks > 0) ? 1u : 0u);
-            }
-            tc_commit_pair_multicast(&sm.empty[stage], 0x3);
+          for (int h = 0; h < 2; ++h) {
+            tmem_cp_pair_32x128b_warpx4(sfw + 4 * h, sfwd + h * kSfChunk);
+            tmem_cp_pair_32x128b_warpx4(sft + 8 * h, sftd + 2 * h * kSfChunk);
+            if (n > 128)
+              tmem_cp_pair_32x128b_warpx4(sft + 8 * h + 4, sftd + (2 * h + 1) * kSfChunk);
           }
-          __syncwarp();
+          const uint64_t wd = w_desc0 + static_cast<uint64_t>(stage) * (kTileBytes >> 4);
+          const uint64_t td = t_desc0 + static_cast<uint64_t>(stage) * (kHalfTok * kKBytes >> 4);
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks) {
+            const uint32_t h = ks >> 1, sf_id = (ks & 1) * 2;
+            mma_mxf4_pair(acc, wd + ks * kKStep, td + ks * kKStep,
+                          idesc0 | (sf_id << 4) | (sf_id << 29), (sfw + 4 * h) | (sf_id << 30),
+                          (sft + 8 * h) | (sf_id << 30), (kb > 0 || ks > 0) ? 1u : 0u);
+          }
+          tc_commit_pair_multicast(&sm.empty[stage], 0x3);
           set ^= 1u;
           if (++stage == kStages) {
             stage = 0;
@@ -250,18 +244,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (!ok) break;
-        if (elect_one()) tc_commit_pair_multicast(&sm.tmem_full, 0x3);
-        __syncwarp();
+        tc_commit_pair_multicast(&sm.tmem_full, 0x3);
         acc_phase ^= 1u;
       }
       // Everything issued above (into both CTAs' TMEM) completes before the pair
       // frees its TMEM.
-      if (elect_one()) {
-        tc_commit_pair_multicast(&sm.drain, 0x1);
-        if (!mbar_wait_limited(&sm.drain, 0, kWaitLimitNs)) atomicOr(p.err, kErrTimeoutBit);
-      }
-      __syncwarp();
+      tc_commit_pair_multicast(&sm.drain, 0x1);
+      if (!mbar_wait_limited(&sm.drain, 0, kWaitLimitNs)) atomicOr(p.err, kErrTimeoutBit);
     }
+    __syncwarp();
   } else if (warp >= 4) {
     // ------------------------------------------------------------- epilogue
     const int q = warp & 3;              // TMEM sub-partition: lanes 32q..32q+31

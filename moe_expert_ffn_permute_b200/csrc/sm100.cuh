@@ -99,19 +99,13 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint32
   }
 }
 
-// The same wait by a whole warp: every lane polls, and the lanes agree on the
-// answer, so the code that follows stays warp-uniform.
-__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, uint32_t* err,
-                                               volatile int* abort_flag) {
-  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, err, abort_flag));
-}
-
 // True on one lane of a converged warp.  A branch on elect.sync tells the
-// compiler that a single thread runs it, so operands that are warp-uniform
-// stay in uniform registers; under `lane == 0` every tensor-core and bulk-copy
-// instruction moves each of its operands there one by one, and an issuing
-// thread measured 58 clocks per tcgen05.cp and 72 per tcgen05.mma.
+// compiler that a single thread runs it, so operands stay in uniform registers;
+// under `lane == 0` every tensor-core and bulk-copy instruction moves each of its
+// operands there one by one, and an issuing thread measured 58 clocks per
+// tcgen05.cp and 72 per tcgen05.mma (about 28 here).  Put the whole issuing loop
+// in the branch: a warp-wide loop that elects a lane per iteration paid 100 more
+// clocks of votes and reconvergence in each.
 __device__ __forceinline__ bool elect_one() {
   uint32_t one;
   asm volatile(
