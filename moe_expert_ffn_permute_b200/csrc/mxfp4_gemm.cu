@@ -25,9 +25,9 @@
 // and the CTA winds down.
 //
 // Few tokens: bound by the weight stream.  One token through 8 experts, 7168 ->
-// 4096, 23.9 us (125 MB, 5.2 TB/s; 1.8 us until the first weights, 1.5 us from the
-// last MMA to the next kernel); a skewed batch of 128 tokens, 28 of 32 experts, 77 us
-// (449 MB, 5.8 TB/s), 71.7 without its MMAs.  Many tokens: operand delivery into
+// 4096, 23.8 us (125 MB, 5.2 TB/s; 1.8 us until the first weights, 1.5 us from the
+// last MMA to the next kernel); a skewed batch of 128 tokens, 28 of 32 experts, 75 us
+// (449 MB, 6.0 TB/s), 70 without its MMAs.  Many tokens: operand delivery into
 // shared memory (52 KB per SM and K block) and then the power cap; mxfp4_pair.cu
 // takes those.
 #include <cuda.h>
