@@ -397,13 +397,19 @@ int tile_cap(int R, int E, int nb_n) {
 }
 
 // CTA pairs (mxfp4_pair.cu) where the average group fills most of a 256-row tile
-// and the 256 x 256 tiles make at least four waves of pairs.  Pairs against this
-// kernel, power-capped, us: 2048 rows per group 7168 -> 4096 x 32 groups 800 / 860,
-// 2048 -> 7168 528 / 545; 256 rows per group 7168 -> 4096 x 32 154 / 162; 192 rows
-// per group 2048 -> 4096 x 64 92 / 88; one group of 4096 rows 4096 -> 4096 (3.5
-// waves) 35.5 / 35.0, of 1024 rows 7168 -> 4096 (under a wave) 17.6 / 15.4.
-bool use_pairs(int R, int E, int N) {
-  return R >= 224ll * E && (R / 256) * ((N + 255ll) / 256) >= 2ll * sm_count();
+// and either K is long (kLongBlocks K blocks) and the 256 x 256 tiles make two
+// waves of pairs, or they make forty.  Pairs against this kernel, power-capped, us:
+//   7168 -> 4096: 2048 rows x 32 groups 827 / 892, 256 x 32 152 / 161, 768 x 4 (2.6
+//   waves) 50 / 53; one group of 1024 rows (under a wave) 17.6 / 15.4
+//   4096 -> 4096: 2048 x 8 134 / 139, 8192 x 1 64 / 64; 2816 -> 4096: 2048 x 8 100 / 105
+//   2048 -> 7168: 2048 x 32 (97 waves) 546 / 566, 1024 x 8 (12 waves) 76.7 / 76.1;
+//   2048 -> 4096: 8192 x 8 (55 waves) 300 / 307, 512 x 64 (27) 195 / 191, 192 x 64
+//   92 / 88; 2048 -> 8192: 4096 x 1 (7 waves) 40 / 38.6
+constexpr int kLongBlocks = 11;
+bool use_pairs(int R, int E, int N, int K) {
+  const long long tiles = (R / 256) * ((N + 255ll) / 256);
+  const int waves = (K + 255) / 256 >= kLongBlocks ? 2 : 40;   // of sm_count() / 2 pairs
+  return R >= 224ll * E && 2 * tiles >= static_cast<long long>(waves) * sm_count();
 }
 
 }  // namespace
@@ -449,7 +455,7 @@ moe_status moe_mxfp4_check_error(const void* workspace, moe_stream_t stream) {
 
 size_t moe_mxfp4_workspace_bytes(int R, int E, int N, int K) {
   if (R < 1 || !moe::mx_gemm_sizes_ok(E, N, K)) return 0;
-  return 256 + (moe::use_pairs(R, E, N) ? moe::mx_pair_record_bytes(R, E, K) : 0);
+  return 256 + (moe::use_pairs(R, E, N, K) ? moe::mx_pair_record_bytes(R, E, K) : 0);
 }
 
 moe_status moe_mxfp4_gemm(const uint8_t* codes, const uint8_t* scales, const int32_t* offsets,
@@ -496,7 +502,7 @@ moe_status moe_mxfp4_gemm(const uint8_t* codes, const uint8_t* scales, const int
   p.cap = moe::tile_cap(R, E, p.nb_n);
   auto st = reinterpret_cast<cudaStream_t>(stream);
   const bool fp16 = dtype == MOE_T_FP16;
-  if (moe::use_pairs(R, E, N)) {
+  if (moe::use_pairs(R, E, N, K)) {
     p.cap = 256;
     return moe::launch_mx_pairs(p, fp16, st) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
   }

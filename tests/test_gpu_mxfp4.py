@@ -214,14 +214,19 @@ def test_product_whole_numbers_bitwise(counts, behind, N, K, dtype):
         assert torch.equal(p(None, dtype), out)       # one group: offsets not needed
 
 
-# Products large enough for the CTA-pair kernel (224 rows per group, four waves of
-# 256 x 256 tiles): halves of 8 to 128 tokens, an odd number of weight blocks (a
-# pair's second block past N), groups without rows, one K block, several tiles per
-# pair.
+# Products on both sides of the CTA-pair kernel's rule (224 rows per group on average,
+# and two waves of 256 x 256 tiles at K > 2560 or forty at less): the first seven run
+# on single CTAs, the others on pairs.  Halves of 8 to 128 tokens, an odd number of
+# weight blocks (a pair's second block past N), groups without rows, one K block, K
+# that ends inside a block, several tiles per pair.  (Whole-number sums reach
+# 144 * 7168 < 2^20 in steps of 2^-4: 24 bits.)
 PAIRS = [
     ([5000], 3, 4104, 32), ([250, 33, 5120, 1, 0], 0, 4096, 96),
     ([1024, 0, 2050, 255, 17], 7, 6280, 288), ([300] * 10, 0, 7048, 160),
     ([2000, 31, 32, 33], 0, 10760, 64), ([77000], 0, 136, 32), ([2600, 700], 0, 6152, 1024),
+    ([5000], 3, 2056, 2848), ([250, 33, 5120, 1, 0], 0, 2048, 2816),
+    ([1024, 0, 2050, 255, 17], 7, 3080, 3104), ([300] * 10, 0, 3592, 2848),
+    ([2000, 31, 32, 33], 0, 5384, 2816), ([2600, 700], 0, 3336, 7168), ([77000], 0, 2456, 32),
 ]
 
 
@@ -276,10 +281,11 @@ def test_product_offsets_that_are_not_prefix_sums():
         assert torch.equal(out.cpu(), want), off
 
 
-def test_product_on_pairs_offsets_and_nan_rows():
-    """Offsets that are not prefix sums, and NaN scales, on the CTA-pair kernel."""
+@pytest.mark.parametrize("N,K", [(5128, 320), (2568, 2848)], ids=["single", "pairs"])
+def test_product_on_pairs_offsets_and_nan_rows(N, K):
+    """Offsets that are not prefix sums, and NaN scales, on large products."""
     ensure_built()
-    R, E, N, K = 4000, 4, 5128, 320
+    R, E = 4000, 4
     a, sa, w, sw = _operands(R, E, N, K, 1, whole=True)
     p = Product(R, E, N, K, a, sa, w, sw)
     av = O.dequantize_mxfp4(a, sa)
@@ -301,11 +307,12 @@ def test_product_on_pairs_offsets_and_nan_rows():
     assert torch.equal(out[~want], clean[~want])
 
 
-def test_product_on_pairs_in_a_graph_beside_another():
-    """A captured pair product (two launches) and a captured small one, workspaces of
-    their own, replayed on two streams at once, equal the eager calls."""
+@pytest.mark.parametrize("N,K", [(5128, 512), (2568, 2816)], ids=["single", "pairs"])
+def test_product_on_pairs_in_a_graph_beside_another(N, K):
+    """A captured large product (two launches on pairs) and a captured small one,
+    workspaces of their own, replayed on two streams at once, equal the eager calls."""
     ensure_built()
-    cases = [([1500, 2500], 5128, 512), ([40] * 32, 256, 1024)]
+    cases = [([1500, 2500], N, K), ([40] * 32, 256, 1024)]
     runs = []
     for i, (counts, N, K) in enumerate(cases):
         p = Product(sum(counts), len(counts), N, K, *_operands(sum(counts), len(counts), N, K, 60 + i))
@@ -534,7 +541,9 @@ def test_product_offsets_past_32_bits(R, E, N, K):
 
 
 @pytest.mark.parametrize("counts,other,N,K", [([40, 0, 9, 15] * 4, [1, 100, 0, 3] * 4, 264, 288),
-                                              ([3000, 1000], [17, 3983], 5128, 64)], ids=["single", "pairs"])
+                                              ([3000, 1000], [17, 3983], 5128, 64),
+                                              ([3000, 1000], [17, 3983], 2568, 2816)],
+                         ids=["single", "single-large", "pairs"])
 def test_replay_on_other_groups(counts, other, N, K):
     """A captured product replayed on other row offsets (and other rows): the launch
     is sized by R and E alone."""
