@@ -385,8 +385,8 @@ moe_status moe_mxfp4_prepack(const uint8_t *w, const uint8_t *w_scales, int E, i
 /* Bytes of moe_mxfp4_gemm's workspace (device, 256-byte aligned); 0 for sizes it
  * does not take; for the current device.  Zero the workspace once before its
  * first use (or moe_mxfp4_clear_error it); calls leave it ready for the next, of
- * the same or other sizes that it is large enough for.  Calls that may overlap on the GPU need workspaces of
- * their own.
+ * the same or other sizes that it is large enough for.  Calls that may overlap on
+ * the GPU need workspaces of their own.
  * No counterpart on the pages.
  */
 size_t moe_mxfp4_workspace_bytes(int R, int E, int N, int K);
