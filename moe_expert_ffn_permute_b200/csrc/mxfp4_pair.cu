@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // past the last one) and stores nothing of it.
         const long long nb = 2ll * t.nb + rank;
         const int block = static_cast<int>((static_cast<long long>(t.e) * p.nb_n + nb) * kb_n);
-        const int row = t.row + rank * (mma_n(t.rows) / 2);
+        const int row = mx::half_row(t.row, mma_n(t.rows), rank, p.R);
         const int rec = static_cast<int>(
             (cluster + static_cast<long long>(i) * clusters) / pairs_n * kb_n);
         for (int kb = 0; kb < kb_n; ++kb) {

@@ -30,6 +30,17 @@ struct Tile {
   int e, nb, row, rows;   // expert, weight block(s), first row, rows (1..cap)
 };
 
+// Token tiles of a group of `rows` rows, at most `cap` tokens each, and the tokens
+// that each of a group's `tiles` tiles has (a multiple of 16; the last may have
+// fewer).  Unsigned: a group may have all of the 2^31 - 1 rows, and the sums that
+// round up pass 2^31 - 1 then.
+__host__ __device__ __forceinline__ int token_tiles(int rows, int cap) {
+  return static_cast<int>((static_cast<uint32_t>(rows) + cap - 1u) / cap);
+}
+__host__ __device__ __forceinline__ int tile_size(int rows, int tiles) {
+  return static_cast<int>(((static_cast<uint32_t>(rows) + tiles - 1u) / tiles + 15u) & ~15u);
+}
+
 // By one whole warp: row offsets clamped to [0, R] and made monotone (a running
 // maximum), so that no content of the array can lead outside the buffers; then
 // the prefix sums of the token tiles, at most `cap` tokens each.
@@ -61,7 +72,7 @@ __device__ __forceinline__ void find_groups(Groups& g, const int32_t* offsets, i
   for (int b = 0; b < E; b += 32) {
     const int i = b + lane;
     const int rows = i < E ? g.row_off[i + 1] - g.row_off[i] : 0;
-    const int own = (rows + cap - 1) / cap;
+    const int own = token_tiles(rows, cap);
     int v = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -91,11 +102,18 @@ __device__ __forceinline__ Tile tile_at(const Groups& g, int E, int nb_n, long l
   t.e = lo;
   const int n = g.row_off[lo + 1] - g.row_off[lo];
   const int tiles = g.tile_off[lo + 1] - g.tile_off[lo];
-  const int size = ((n + tiles - 1) / tiles + 15) & ~15;
+  const int size = tile_size(n, tiles);
   const int local = (tt - g.tile_off[lo]) * size;
   t.row = g.row_off[lo] + local;
   t.rows = min(size, n - local);
   return t;
+}
+
+// First row of a half (0 or 1) of a tile whose MMA has n columns; past the last
+// row it is R, whose rows arrive as zeros (t.row + n / 2 may pass 2^31 - 1).
+__host__ __device__ __forceinline__ int half_row(int row, int n, int half, int R) {
+  const uint32_t first = static_cast<uint32_t>(row) + static_cast<uint32_t>(half * (n / 2));
+  return static_cast<int>(first < static_cast<uint32_t>(R) ? first : static_cast<uint32_t>(R));
 }
 
 // Two fp32 -> two 16-bit floats, round to nearest even; `lo` in the low half.

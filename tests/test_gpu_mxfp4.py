@@ -601,3 +601,40 @@ def test_operators_on_a_plan_s_routing():
         res.append((codes, scales, out, rows))
     assert all(torch.equal(a, b) for a, b in zip(*res))
     assert lay.check() == 0
+
+
+def test_product_of_the_most_rows():
+    """2^31 - 1 rows (95 GB of buffers), in one group and with a last group of a single
+    row whose second half would lie past 2^31 - 1: every row written, bitwise."""
+    ensure_built()
+    R, E, N, K = (1 << 31) - 1, 2, 8, 32
+    torch.cuda.empty_cache()
+    g = _gen(21)
+    codes = torch.randint(0, 256, (R, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    scales = torch.zeros(1, R, 4, dtype=torch.uint8, device="cuda")
+    scales[:, :, 0] = 127
+    w = torch.randint(0, 256, (E, N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    ws = torch.full((E, N, 1), 127, dtype=torch.uint8, device="cuda")
+    out = torch.empty(R, N, dtype=torch.bfloat16, device="cuda")
+    table = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], device="cuda")
+    table = torch.cat([table, -table])
+    value = lambda c: table[torch.stack([c & 15, c >> 4], -1).flatten(-2).int()]  # noqa: E731
+    for counts in ([R], [R - 1, 1]):
+        n = len(counts)
+        wt = torch.empty(moe.moe_mxfp4_weight_bytes(n, N, K), dtype=torch.uint8, device="cuda")
+        st = torch.empty(moe.moe_mxfp4_weight_scale_bytes(n, N, K), dtype=torch.uint8, device="cuda")
+        moe.moe_mxfp4_prepack(w[:n], ws[:n], n, N, K, wt, st)
+        space = torch.zeros(moe.moe_mxfp4_workspace_bytes(R, n, N, K), dtype=torch.uint8, device="cuda")
+        out.fill_(float("nan"))
+        off = _cuda(_offsets(np.array(counts, np.int64)))
+        moe.moe_mxfp4_gemm(codes, scales, off, R, n, N, K, wt, st, "bf16", out, space)
+        assert moe.moe_mxfp4_check_error(space) == 0
+        del space
+        step = 1 << 24
+        for e, lo, hi in ((0, 0, counts[0]),) + (((1, R - 1, R),) if n == 2 else ()):
+            for r in range(lo, hi, step):
+                rows = slice(r, min(r + step, hi))
+                want = (value(codes[rows]) @ value(w[e]).T).bfloat16()      # exact in fp32
+                assert torch.equal(out[rows], want), (n, r)
+    del codes, scales, out
+    torch.cuda.empty_cache()
