@@ -409,6 +409,16 @@ moe_status moe_mxfp4_gemm(const uint8_t *codes, const uint8_t *scales, const int
                           const uint8_t *w_scales_chunked, int dtype, void *out,
                           void *workspace, moe_stream_t stream);
 
+/* Test hook for the failure path, 0 by default and of the calling thread alone.
+ * Bit 0: in every product that this thread launches from now on the tensor-core
+ * issuers wait for an arrival that never comes, so that bounded wait (and those
+ * that depend on it) runs out after about 2 s: the launch stops, the workspace's
+ * error word gets MOE_ERR_DEVICE_TIMEOUT, nothing traps or hangs, and out is
+ * undefined.  Other bits: MOE_ERR_INVALID_ARG.
+ * No counterpart on the pages.
+ */
+moe_status moe_mxfp4_set_debug(int flags);
+
 /* Make the workspace ready again after a device-side error (enqueued on
  * `stream`), and read its error word: the latter synchronises `stream` and
  * returns MOE_OK or MOE_ERR_DEVICE_TIMEOUT.

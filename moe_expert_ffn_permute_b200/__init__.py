@@ -94,6 +94,7 @@ _SIGS = {
     "moe_mxfp4_prepack": (ctypes.c_int, [_P] * 2 + [_I] * 3 + [_P] * 3),
     "moe_mxfp4_workspace_bytes": (ctypes.c_size_t, [_I] * 4),
     "moe_mxfp4_gemm": (ctypes.c_int, [_P] * 3 + [_I] * 4 + [_P] * 2 + [_I] + [_P] * 3),
+    "moe_mxfp4_set_debug": (ctypes.c_int, [_I]),
     "moe_mxfp4_clear_error": (ctypes.c_int, [_P] * 2),
     "moe_mxfp4_check_error": (ctypes.c_int, [_P] * 2),
 }
@@ -628,6 +629,12 @@ def moe_mxfp4_gemm(codes, scales, offsets, R, E, N, K, w_tiled, w_scales_chunked
         _buf(fn, "out", out, R * N * z, tt, at), _buf(fn, "workspace", workspace, need, None, at), st)
     if status:
         raise MoEError(status, fn)
+
+
+def moe_mxfp4_set_debug(flags):
+    """Bit 0 (or True): the failure-path test hook, for products that this thread
+    launches (the issuers' wait runs out)."""
+    _check(lib().moe_mxfp4_set_debug(int(flags)), "moe_mxfp4_set_debug")
 
 
 def moe_mxfp4_clear_error(workspace, stream=None):

@@ -175,9 +175,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      // On the way out of an aborted CTA: its copies in flight land before its
-      // shared memory is given back.
-      for (int s = 0; !ok && s < STAGES && s < issued; ++s) {
+      // The copies land before the CTA gives its shared memory back, also where
+      // it was another warp that gave up (else they have landed long since).
+      for (int s = 0; s < STAGES && s < issued; ++s) {
         if (--stage < 0) {
           stage = STAGES - 1;
           phase ^= 1u;
@@ -222,6 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // No copy of this thread is in flight when the CTA ends.
     asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();   // (lanes may leave an aborted loop apart)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issue
     if (elect_one()) {
@@ -233,7 +234,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t sfw_desc0 = sf_desc(smem_u32(sm.sfw[0]));
       const uint64_t sft_desc0 = sf_desc(smem_u32(sm.sft[0]));
       constexpr uint64_t kKStep = 32 >> 4, kSfChunk = 512 >> 4;
-      bool ok = true;
+      // (Nothing arrives on `drain` before the end of this branch.)
+      bool ok = p.fault == 0 || mbar_wait(&sm.drain, 0, p.err, &sm.abort_flag);
       for (int i = 0; ok && i < my_tiles; ++i) {
         const Tile t =
             tile_at(sm.groups, p.E, p.nb_n, blockIdx.x + static_cast<long long>(i) * gridDim.x);
@@ -302,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tile_at(sm.groups, p.E, p.nb_n, blockIdx.x + static_cast<long long>(i) * gridDim.x);
       const int n = static_cast<int>(mma_n(t.rows));
       const int c0 = mx::half_begin(n, half), cols = half ? n - c0 : mx::half_begin(n, 1);
-      if (!mbar_wait(&sm.tmem_full, acc_phase, p.err, &sm.abort_flag)) break;
+      if (!mbar_wait_warp(&sm.tmem_full, acc_phase, p.err, &sm.abort_flag)) break;
       acc_phase ^= 1u;
       tc_fence_after();
       // (kCols columns are loaded whatever the tile holds: they are always
@@ -329,6 +331,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // --------------------------------------------------------------- host side
+thread_local int g_debug_fault = 0;   // moe_mxfp4_set_debug
+
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                    const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                                    const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -434,6 +438,12 @@ bool mx::map_rows(CUtensorMap* m, const void* base, uint64_t width, uint64_t row
 
 extern "C" {
 
+moe_status moe_mxfp4_set_debug(int flags) {
+  if (flags & ~1) return MOE_ERR_INVALID_ARG;
+  moe::g_debug_fault = flags & 1;
+  return MOE_OK;
+}
+
 moe_status moe_mxfp4_clear_error(void* workspace, moe_stream_t stream) {
   if (workspace == nullptr) return MOE_ERR_INVALID_ARG;
   if (!moe::aligned_to(workspace, 256)) return MOE_ERR_ALIGNMENT;
@@ -499,6 +509,7 @@ moe_status moe_mxfp4_gemm(const uint8_t* codes, const uint8_t* scales, const int
   p.out = static_cast<uint16_t*>(out);
   p.err = static_cast<uint32_t*>(workspace);
   p.records = static_cast<uint8_t*>(workspace) + 256;
+  p.fault = moe::g_debug_fault;
   p.cap = moe::tile_cap(R, E, p.nb_n);
   auto st = reinterpret_cast<cudaStream_t>(stream);
   const bool fp16 = dtype == MOE_T_FP16;

@@ -184,13 +184,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (!ok) {
-        // On the way out of an aborted pair: the copies in flight (microseconds)
-        // land before the shared memory is given back.  Their barrier is the
-        // leader's and may never complete, so this waits by time.
-        const uint64_t t0 = globaltimer();
-        while (globaltimer() - t0 < 1000000ull) __nanosleep(1000);
-      }
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -204,7 +197,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t sfw_desc0 = sf_desc(smem_u32(sm.sfw[0]));
       const uint64_t sft_desc0 = sf_desc(smem_u32(sm.sft[0]));
       constexpr uint64_t kKStep = 32 >> 4, kSfChunk = 512 >> 4;
-      bool ok = true;
+      // (Nothing arrives on `drain` before the end of this branch.)
+      bool ok = p.fault == 0 || mbar_wait(&sm.drain, 0, p.err, &sm.abort_flag);
       for (int i = 0; ok && i < my_tiles; ++i) {
         const uint32_t n = static_cast<uint32_t>(mma_n(tile(i).rows));
         const uint32_t idesc0 = mxf4_idesc_m256(n, 0);
@@ -265,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Tile t = tile(i);
       const int n = mma_n(t.rows);
       const int c0 = mx::half_begin(n, half), cols = half ? n - c0 : mx::half_begin(n, 1);
-      if (!mbar_wait(&sm.tmem_full, acc_phase, p.err, &sm.abort_flag)) break;
+      if (!mbar_wait_warp(&sm.tmem_full, acc_phase, p.err, &sm.abort_flag)) break;
       acc_phase ^= 1u;
       tc_fence_after();
       uint32_t v[kCols];
@@ -282,6 +276,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
+  if (sm.abort_flag) {
+    // Copies in flight (microseconds) land before the shared memory is given back,
+    // whichever warp gave up.  Their barrier is the leader's and may never
+    // complete, so this waits by time.
+    const uint64_t t0 = globaltimer();
+    while (globaltimer() - t0 < 1000000ull) __nanosleep(1000);
+    __syncthreads();
+  }
   cluster_sync();   // no remote operation targets a CTA that has left
   if (warp == 1) {
     tc_fence_after();

@@ -175,6 +175,7 @@ struct MxGemm {
   int R, E, N, K;
   int cap;                    // most tokens of a tile (a multiple of 16)
   int nb_n, kb_n;             // 128-row weight blocks, 256-wide K blocks
+  int fault;                  // test hook: the MMA issuers wait for what never comes
   const int32_t* offsets;     // null: one group of all rows
   const uint8_t* codes;
   const uint8_t* scales;      // token scales, group-major [ceil(K/128)][R][4]

@@ -99,6 +99,14 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint32
   }
 }
 
+// The same wait by a whole converged warp, with one answer for all its lanes: at
+// the limit some may see the phase complete where others gave up, and the
+// warp-wide loads and shuffles behind a wait need every lane.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, uint32_t* err,
+                                               volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, err, abort_flag));
+}
+
 // True on one lane of a converged warp.  A branch on elect.sync tells the
 // compiler that a single thread runs it, so operands stay in uniform registers;
 // under `lane == 0` every tensor-core and bulk-copy instruction moves each of its

@@ -638,3 +638,54 @@ def test_product_of_the_most_rows():
                 assert torch.equal(out[rows], want), (n, r)
     del codes, scales, out
     torch.cuda.empty_cache()
+
+
+# One product for each kernel: groups of few rows, of more, and on CTA pairs.
+VARIANTS = [([40, 0, 9, 15] * 4, 264, 288), ([300, 500], 264, 288), ([1500, 2500], 2568, 2816)]
+
+
+@pytest.mark.timeout(120)
+@pytest.mark.parametrize("counts,N,K", VARIANTS, ids=["few", "many", "pairs"])
+def test_waits_that_run_out_end_the_product(counts, N, K):
+    """The issuers' wait runs out (debug hook): the launch stops with a timeout in the
+    workspace's error word, the context stays usable, and the word stays until it is
+    cleared."""
+    ensure_built()
+    E, R = len(counts), sum(counts)
+    a, sa, w, sw = _operands(R, E, N, K, 31, whole=True)
+    off = _cuda(_offsets(counts))
+    p = Product(R, E, N, K, a, sa, w, sw)
+    assert (p.workspace.numel() > 256) == (R == 4000)
+    want = p(off, "bf16")
+    p.check()
+    try:
+        moe.moe_mxfp4_set_debug(1)
+        p(off, "bf16")
+        torch.cuda.synchronize()
+    finally:
+        moe.moe_mxfp4_set_debug(0)
+    assert moe.moe_mxfp4_check_error(p.workspace) == 5          # MOE_ERR_DEVICE_TIMEOUT
+    assert torch.equal(p(off, "bf16"), want)
+    assert moe.moe_mxfp4_check_error(p.workspace) == 5
+    moe.moe_mxfp4_clear_error(p.workspace)
+    assert torch.equal(p(off, "bf16"), want)
+    p.check()
+
+
+def test_error_word_is_read_and_cleared():
+    """The error word as the kernels write it (bit 5), written from the host."""
+    ensure_built()
+    counts, N, K = VARIANTS[0]
+    E, R = len(counts), sum(counts)
+    p = Product(R, E, N, K, *_operands(R, E, N, K, 33, whole=True))
+    off = _cuda(_offsets(counts))
+    want = p(off, "bf16")
+    p.check()
+    p.workspace[:4] = torch.tensor([32, 0, 0, 0], dtype=torch.uint8, device="cuda")
+    assert moe.moe_mxfp4_check_error(p.workspace) == 5
+    assert torch.equal(p(off, "bf16"), want)
+    assert moe.moe_mxfp4_check_error(p.workspace) == 5
+    moe.moe_mxfp4_clear_error(p.workspace)
+    p.check()
+    assert torch.equal(p(off, "bf16"), want)
+    p.check()

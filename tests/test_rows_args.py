@@ -149,3 +149,11 @@ def test_sizes_of_prepacked_weights():
         assert moe.moe_mxfp4_workspace_bytes(4, E, N, K) == 0
     assert moe.moe_mxfp4_workspace_bytes(0, 1, 128, 256) == 0
     assert moe.moe_mxfp4_workspace_bytes(1, 1, 128, 256) >= 256
+
+
+def test_debug_flags_of_the_product():
+    for flags in (2, -1, 1 << 20):
+        with pytest.raises(moe.MoEError) as e:
+            moe.moe_mxfp4_set_debug(flags)
+        assert e.value.status == INVALID
+    moe.moe_mxfp4_set_debug(0)
