@@ -11,6 +11,7 @@ function is first called: there is no fallback implementation.
 import ctypes
 import math
 import os
+from operator import index
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe_b200.so")
@@ -418,8 +419,12 @@ def moe_forward_launch_count(plan):
 
 
 def _sizes(fn, *values):
-    """Refuses a call whose sizes are negative or would wrap around as C ints."""
-    raise MoEError(MOE_ERR_INVALID_ARG, f"{fn}: sizes {values} must be C ints of at least 0")
+    """Sizes as Python ints.  (Those of NumPy wrap around in their own arithmetic, and a
+    buffer's length with them.)  Refuses sizes that are negative or no C ints."""
+    sizes = [index(v) for v in values]
+    if any(v >> 31 for v in sizes):
+        raise MoEError(MOE_ERR_INVALID_ARG, f"{fn}: sizes {sizes} must be C ints of at least 0")
+    return sizes
 
 
 def _choice(fn, name, table, value):
@@ -456,8 +461,11 @@ def _buf(fn, name, t, nbytes, dtype, device):
 def moe_permute(x, T, row_bytes, k, inv, rows, stream=None):
     """rows[inv[t, j]] = x[t]: x [T, row_bytes] of any type -> rows [T*k, row_bytes]."""
     fn = "moe_permute"
-    if (T | k) >> 31:
-        _sizes(fn, T, k)
+    n = T | k
+    if type(n) is not int or n >> 31:
+        T, k = _sizes(fn, T, k)
+    if type(row_bytes) is not int:
+        row_bytes = index(row_bytes)
     at, st = _here(stream)
     S = T * k
     status = (_lib or lib()).moe_permute(
@@ -472,8 +480,9 @@ def moe_permute_backward(drows, dtype, T, H, k, inv, dx, stream=None):
     fn = "moe_permute_backward"
     if dtype not in _ELEM:
         _choice(fn, "dtype", _ELEM, dtype)
-    if (T | H | k) >> 31:
-        _sizes(fn, T, H, k)
+    n = T | H | k
+    if type(n) is not int or n >> 31:
+        T, H, k = _sizes(fn, T, H, k)
     at, st = _here(stream)
     d, z, tt = _ELEM[dtype]
     S = T * k
@@ -489,8 +498,9 @@ def moe_unpermute(rows, dtype, T, H, k, inv, topk_w, out, stream=None):
     fn = "moe_unpermute"
     if dtype not in _ELEM:
         _choice(fn, "dtype", _ELEM, dtype)
-    if (T | H | k) >> 31:
-        _sizes(fn, T, H, k)
+    n = T | H | k
+    if type(n) is not int or n >> 31:
+        T, H, k = _sizes(fn, T, H, k)
     at, st = _here(stream)
     d, z, tt = _ELEM[dtype]
     S = T * k
@@ -507,8 +517,9 @@ def moe_unpermute_backward(dout, rows, dtype, T, H, k, inv, topk_w, drows, dw, s
     fn = "moe_unpermute_backward"
     if dtype not in _ELEM:
         _choice(fn, "dtype", _ELEM, dtype)
-    if (T | H | k) >> 31:
-        _sizes(fn, T, H, k)
+    n = T | H | k
+    if type(n) is not int or n >> 31:
+        T, H, k = _sizes(fn, T, H, k)
     at, st = _here(stream)
     d, z, tt = _ELEM[dtype]
     S = T * k
@@ -537,8 +548,9 @@ def moe_quantize_mxfp4(x, dtype, T, K, k, inv, codes, scales, scale_layout="row"
         _choice(fn, "dtype", _ELEM, dtype)
     if scale_layout not in SCALE_LAYOUTS:
         _choice(fn, "scale_layout", SCALE_LAYOUTS, scale_layout)
-    if (T | K | k) >> 31:
-        _sizes(fn, T, K, k)
+    n = T | K | k
+    if type(n) is not int or n >> 31:
+        T, K, k = _sizes(fn, T, K, k)
     at, st = _here(stream)
     d, z, tt = _ELEM[dtype]
     s = SCALE_LAYOUTS[scale_layout]
@@ -558,8 +570,9 @@ def moe_dequantize_mxfp4(codes, scales, scale_layout, R, K, dtype, out, stream=N
         _choice(fn, "dtype", _ELEM, dtype)
     if scale_layout not in SCALE_LAYOUTS:
         _choice(fn, "scale_layout", SCALE_LAYOUTS, scale_layout)
-    if (R | K) >> 31:
-        _sizes(fn, R, K)
+    n = R | K
+    if type(n) is not int or n >> 31:
+        R, K = _sizes(fn, R, K)
     at, st = _here(stream)
     d, z, tt = _ELEM[dtype]
     s = SCALE_LAYOUTS[scale_layout]
@@ -588,8 +601,9 @@ def _weight_tiles(E, N, K):
 def moe_mxfp4_prepack(w, w_scales, E, N, K, w_tiled, w_scales_chunked, stream=None):
     """Weights u8 [E, N, K/2] and scales u8 [E, N, K/32] -> the layout moe_mxfp4_gemm reads."""
     fn = "moe_mxfp4_prepack"
-    if (E | N | K) >> 31:
-        _sizes(fn, E, N, K)
+    n = E | N | K
+    if type(n) is not int or n >> 31:
+        E, N, K = _sizes(fn, E, N, K)
     at, st = _here(stream)
     tiles = _weight_tiles(E, N, K)
     _check(lib().moe_mxfp4_prepack(
@@ -612,8 +626,9 @@ def moe_mxfp4_gemm(codes, scales, offsets, R, E, N, K, w_tiled, w_scales_chunked
     fn = "moe_mxfp4_gemm"
     if dtype not in _ELEM:
         _choice(fn, "dtype", _ELEM, dtype)
-    if (R | E | N | K) >> 31:
-        _sizes(fn, R, E, N, K)
+    n = R | E | N | K
+    if type(n) is not int or n >> 31:
+        R, E, N, K = _sizes(fn, R, E, N, K)
     at, st = _here(stream)
     d, z, tt = _ELEM[dtype]
     tiles = _weight_tiles(E, N, K)

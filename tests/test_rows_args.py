@@ -157,3 +157,51 @@ def test_debug_flags_of_the_product():
             moe.moe_mxfp4_set_debug(flags)
         assert e.value.status == INVALID
     moe.moe_mxfp4_set_debug(0)
+
+
+# Sizes whose products pass 2^31, as NumPy integers of 32 bits: in their own arithmetic
+# the buffers' lengths would wrap around to zero and short tensors pass for whole ones.
+WRAPPING = [
+    ("moe_permute", dict(x="u8", T=1 << 12, row_bytes=1 << 20, k=2, inv="i32", rows="u8"), "x"),
+    ("moe_permute_backward", dict(drows="bf16", dtype="bf16", T=1 << 12, H=1 << 19, k=2, inv="i32",
+                                  dx="bf16"), "drows"),
+    ("moe_unpermute", dict(rows="bf16", dtype="bf16", T=1 << 12, H=1 << 19, k=2, inv="i32",
+                           topk_w="f32", out="bf16"), "rows"),
+    ("moe_unpermute_backward", dict(dout="bf16", rows="bf16", dtype="bf16", T=1 << 12, H=1 << 19, k=2,
+                                    inv="i32", topk_w="f32", drows="bf16", dw="f32"), "dout"),
+    ("moe_quantize_mxfp4", dict(x="bf16", dtype="bf16", T=1 << 12, K=1 << 21, k=1, inv=None, codes="u8",
+                                scales="u8", scale_layout="group"), "x"),
+    ("moe_dequantize_mxfp4", dict(codes="u8", scales="u8", scale_layout="row", R=1 << 12, K=1 << 25,
+                                  dtype="bf16", out="bf16"), "codes"),
+    ("moe_mxfp4_prepack", dict(w="u8", w_scales="u8", E=1 << 8, N=1 << 10, K=1 << 15, w_tiled="u8",
+                               w_scales_chunked="u8"), "w"),
+    ("moe_mxfp4_gemm", dict(codes="u8", scales="u8", offsets="i32", R=1 << 20, E=2, N=1 << 12, K=1 << 13,
+                            w_tiled="u8", w_scales_chunked="u8", dtype="bf16", out="bf16",
+                            workspace="u8"), "codes"),
+]
+
+
+@pytest.mark.parametrize("fn,args,first", WRAPPING, ids=[w[0][4:] for w in WRAPPING])
+def test_sizes_as_numpy_integers_do_not_wrap(fn, args, first, monkeypatch):
+    import numpy as np
+    monkeypatch.setattr(moe, "_here", lambda stream: (-1, 0))      # tensors of the CPU pass for the GPU's
+    kinds = {"u8": torch.uint8, "i32": torch.int32, "f32": torch.float32, "bf16": torch.bfloat16}
+    long = [a for a, v in args.items() if v in ("i32", "f32")]
+    call = {a: torch.zeros(1 << 14 if a in long else 64, dtype=kinds[v]) if v in kinds and a != "dtype" else v
+            for a, v in args.items()}
+    for a, v in args.items():
+        if isinstance(v, int):
+            call[a] = np.int32(v)
+    with pytest.raises(moe.MoEError) as e:
+        getattr(moe, fn)(**call)
+    assert e.value.status == INVALID and f"{first} holds" in str(e.value), e.value
+
+
+def test_sizes_as_numpy_integers_are_taken():
+    import numpy as np
+    for n in (np.int32, np.int64, np.uint8, torch.tensor):
+        _refused(UNSUPPORTED, "moe_unpermute", T=n(4), H=n(20), k=n(2))
+        _refused(UNSUPPORTED, "moe_mxfp4_gemm", R=n(8), K=n(48))
+        _refused(INVALID, "moe_permute", T=n(0))
+    _refused(INVALID, "moe_unpermute", T=np.int64(1 << 31))
+    _refused(INVALID, "moe_unpermute", H=np.int64(-8))
