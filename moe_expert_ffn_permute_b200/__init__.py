@@ -464,8 +464,11 @@ def moe_permute(x, T, row_bytes, k, inv, rows, stream=None):
     n = T | k
     if type(n) is not int or n >> 31:
         T, k = _sizes(fn, T, k)
-    if type(row_bytes) is not int:
+    if type(row_bytes) is not int or row_bytes >> 63:
         row_bytes = index(row_bytes)
+        if row_bytes >> 63:
+            raise MoEError(MOE_ERR_INVALID_ARG, f"{fn}: row_bytes {row_bytes} must be a 64-bit int of "
+                                                "at least 0")
     at, st = _here(stream)
     S = T * k
     status = (_lib or lib()).moe_permute(

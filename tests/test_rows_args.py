@@ -205,3 +205,9 @@ def test_sizes_as_numpy_integers_are_taken():
         _refused(INVALID, "moe_permute", T=n(0))
     _refused(INVALID, "moe_unpermute", T=np.int64(1 << 31))
     _refused(INVALID, "moe_unpermute", H=np.int64(-8))
+
+
+def test_row_bytes_past_64_bits_are_refused():
+    """(1 << 64) + 255 would reach the library as 255, a size it refuses for another reason."""
+    for row_bytes in ((1 << 64) + 255, (1 << 63) + 1, -(1 << 64) + 255, -4):
+        _refused(INVALID, "moe_permute", row_bytes=row_bytes)
