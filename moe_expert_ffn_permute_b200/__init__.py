@@ -656,12 +656,17 @@ def moe_mxfp4_set_debug(flags):
 
 
 def moe_mxfp4_clear_error(workspace, stream=None):
-    _check(lib().moe_mxfp4_clear_error(_ptr(workspace), _stream(stream)), "moe_mxfp4_clear_error")
+    """Zeroes the error word's 256 bytes."""
+    fn = "moe_mxfp4_clear_error"
+    at, st = _here(stream)
+    _check(lib().moe_mxfp4_clear_error(_buf(fn, "workspace", workspace, 256, None, at), st), fn)
 
 
 def moe_mxfp4_check_error(workspace, stream=None):
     """Synchronises the stream; returns the moe_status code (0 = no device error)."""
-    return lib().moe_mxfp4_check_error(_ptr(workspace), _stream(stream))
+    at, st = _here(stream)
+    return lib().moe_mxfp4_check_error(
+        _buf("moe_mxfp4_check_error", "workspace", workspace, 256, None, at), st)
 
 
 def _expect(name, t, shape, dtype, device):

@@ -211,3 +211,17 @@ def test_row_bytes_past_64_bits_are_refused():
     """(1 << 64) + 255 would reach the library as 255, a size it refuses for another reason."""
     for row_bytes in ((1 << 64) + 255, (1 << 63) + 1, -(1 << 64) + 255, -4):
         _refused(INVALID, "moe_permute", row_bytes=row_bytes)
+
+
+@pytest.mark.parametrize("fn", [moe.moe_mxfp4_clear_error, moe.moe_mxfp4_check_error],
+                         ids=["clear", "check"])
+def test_error_word_of_a_tensor_that_is_no_workspace(fn, monkeypatch):
+    """One on the CPU, one shorter than the 256 bytes that are written, one with gaps."""
+    with pytest.raises(moe.MoEError) as e:
+        fn(torch.zeros(256, dtype=torch.uint8))
+    assert e.value.status == INVALID
+    monkeypatch.setattr(moe, "_here", lambda stream: (-1, 0))      # tensors of the CPU pass for the GPU's
+    for t in (torch.zeros(255, dtype=torch.uint8), torch.zeros(512, dtype=torch.uint8)[::2]):
+        with pytest.raises(moe.MoEError) as e:
+            fn(t)
+        assert e.value.status == INVALID
