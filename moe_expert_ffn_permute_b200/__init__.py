@@ -536,6 +536,8 @@ def moe_unpermute_backward(dout, rows, dtype, T, H, k, inv, topk_w, drows, dw, s
 
 def mxfp4_scale_shape(R, K, layout):
     """Shape of the scale bytes of R rows of K elements, layout "row" or "group"."""
+    if layout not in SCALE_LAYOUTS:
+        _choice("mxfp4_scale_shape", "layout", SCALE_LAYOUTS, layout)
     return (R, K // 32) if layout == "row" else ((K + 127) // 128, R, 4)
 
 

@@ -225,3 +225,12 @@ def test_error_word_of_a_tensor_that_is_no_workspace(fn, monkeypatch):
         with pytest.raises(moe.MoEError) as e:
             fn(t)
         assert e.value.status == INVALID
+
+
+def test_scale_shapes():
+    assert moe.mxfp4_scale_shape(5, 288, "row") == (5, 9)
+    assert moe.mxfp4_scale_shape(5, 288, "group") == (3, 5, 4)
+    for layout in ("rows", "row-major", 0, None):
+        with pytest.raises(moe.MoEError) as e:
+            moe.mxfp4_scale_shape(5, 288, layout)
+        assert e.value.status == INVALID
