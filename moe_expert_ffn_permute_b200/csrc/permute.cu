@@ -261,18 +261,17 @@ cudaError_t launch_backward(const void* dout, const void* rows, const int32_t* i
 
 // Slots of a token that a block of the gradient takes: four (4096 tokens, top-8,
 // 7168 wide in bf16: 150 us; eight take 163, their 109 registers leave few blocks
-// per SM; two 171, one 173, re-reading dout), or one below this many tokens, where
-// a token's slots should spread over the SMs (one slot / four, same width: 37
+// per SM; two 171, one 173, re-reading dout), or one below two tokens per SM, where
+// a token's slots should spread over the SMs (148 SMs, one slot / four, same width: 37
 // tokens 3.4 / 5.4 us, 200 8.5 / 10.4, 296 11.5 / 12.1, 400 15.0 / 13.7; rows of
 // 6 KB cross over earlier, at most 0.6 us apart).
 constexpr int kBackSlots = 4;
-constexpr int kSlotBlocksBelow = 2 * 148;
 
 template <int kDtype>
 cudaError_t launch_backward_any(const void* dout, const void* rows, const int32_t* inv,
                                 const float* topk_w, int T, long long vecs, int k, void* drows,
                                 float* dw, cudaStream_t st) {
-  if (T < kSlotBlocksBelow || k == 1)
+  if (T < 2 * sm_count() || k == 1)
     return launch_backward<kDtype, 1>(dout, rows, inv, topk_w, T, vecs, k, drows, dw, st);
   return launch_backward<kDtype, kBackSlots>(dout, rows, inv, topk_w, T, vecs, k, drows, dw, st);
 }
