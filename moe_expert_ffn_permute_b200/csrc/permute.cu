@@ -24,8 +24,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kSlotGroup = 8;   // slots whose stores the copy issues together
-// Slots whose rows the sum loads together (8192 tokens, top-8, 7168 wide: 158 us;
-// eight take 170, their 114 registers leave two blocks per SM).
+// Slots whose rows the sum loads together (8192 tokens, top-8, 7168 wide: 152 us;
+// eight take 157, their 114 registers leave two blocks per SM; two 155).
 constexpr int kSumGroup = 4;
 // 16-byte chunks of a row per thread of the copy and the sum (one in each half
 // of the row), as in the layer's combine.
@@ -70,8 +70,8 @@ __global__ void __launch_bounds__(kThreads) permute_kernel(const V* __restrict__
 
 // The same thread layout the other way round: kSumGroup rows' chunks are loaded
 // together and summed in fp32, j ascending.  topk_w == nullptr: weights 1.  Bound
-// by the reads: the copy's size above, 5% of the slots masked, takes 156 us, 6.5
-// TB/s of its 1.01 GB.
+// by the reads: the copy's size above, 5% of the slots masked, takes 152 us, 6.65
+// TB/s of its 1.01 GB (156 where one of a thread's two stores does not stream).
 template <int kDtype>
 __global__ void __launch_bounds__(kThreads) unpermute_kernel(
     const uint4* __restrict__ rows, const int32_t* __restrict__ inv,
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kThreads) unpermute_kernel(
     }
   }
   __stcs(out + t * vecs + c, E::pack(acc[0]));
-  if (second) out[t * vecs + c + half] = E::pack(acc[1]);
+  if (second) __stcs(out + t * vecs + c + half, E::pack(acc[1]));
 }
 
 // One block per (token, group of kJ slots): dout's row is read once for the
