@@ -7,6 +7,10 @@ sum, ceil(K / 64) times.  Taking each of those additions to keep 24 bits, rounde
 or cut (2^-23 relative to the magnitudes added), the sum is off by at most
 (64 + K / 64) * 2^-23 * sum |a w|; then one rounding to the output type (bf16
 2^-8, fp16 2^-11).  Whole-number cases, whose sums fit 24 bits, are bitwise."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -689,3 +693,95 @@ def test_error_word_is_read_and_cleared():
     p.check()
     assert torch.equal(p(off, "bf16"), want)
     p.check()
+
+
+# Sizes on pairs (the last of VARIANTS) and on single CTAs, with the kernel that takes them.
+def _on_pairs(R, E, N, K):
+    return moe.moe_mxfp4_workspace_bytes(R, E, N, K) > 256
+
+
+def test_cases_reach_the_kernels_they_are_for():
+    """PRODUCTS and the first seven of PAIRS run on single CTAs, the others on pairs."""
+    ensure_built()
+    sizes = [(sum(c) + b, len(c), N, K) for c, b, N, K in PRODUCTS + PAIRS]
+    assert [_on_pairs(*s) for s in sizes] == [False] * (len(PRODUCTS) + 7) + [True] * (len(PAIRS) - 7)
+
+
+@pytest.mark.parametrize("shift", [-125, -93, 93, 125])
+@pytest.mark.parametrize("counts,N,K", VARIANTS, ids=["few", "many", "pairs"])
+def test_product_of_distant_scales_bitwise(counts, N, K, shift):
+    """Scale bytes from 1 to 253 on one side and as far from 127 the other way on the
+    other: the products of two scales are 2^-2 to 2^2, and the sums exact."""
+    ensure_built()
+    E, R = len(counts), sum(counts)
+    a, sa, w, sw = _operands(R, E, N, K, 71, whole=True)
+    sa, sw = (sa.astype(int) + shift).astype(np.uint8), (sw.astype(int) - shift).astype(np.uint8)
+    off = _offsets(counts)
+    p = Product(R, E, N, K, a, sa, w, sw)
+    assert _on_pairs(R, E, N, K) == (R == 4000)
+    want = O.grouped_product(O.dequantize_mxfp4(a, sa), O.dequantize_mxfp4(w.reshape(E * N, -1),
+                             sw.reshape(E * N, -1)).reshape(E, N, K), off, np.full((R, N), 7.0))
+    for dtype in ("bf16", "fp16"):
+        out = p(_cuda(off), dtype)
+        p.check()
+        assert torch.equal(out.cpu(), torch.from_numpy(want).to(DT[dtype]))
+
+
+@pytest.mark.parametrize("counts,behind,N,K", [([1400, 0, 2600], 2, 2568, 2848), ([3000], 0, 4104, 7168),
+                                               ([300] * 6, 1, 6152, 2912)])
+def test_product_on_pairs_of_quantised_values(counts, behind, N, K):
+    ensure_built()
+    assert _on_pairs(sum(counts) + behind, len(counts), N, K)
+    test_product_of_quantised_values(counts, behind, N, K)
+
+
+def test_product_codes_past_32_bits_on_single_ctas():
+    ensure_built()
+    assert not _on_pairs(57000, 256, 8, 151552)
+    test_product_offsets_past_32_bits(57000, 256, 8, 151552)
+
+
+FIRST_CALLS = """
+import sys
+import torch
+sys.path[:0] = [{root!r}, {root!r} + "/tests"]
+import moe_expert_ffn_permute_b200 as moe
+u8, bf16 = torch.uint8, torch.bfloat16
+rnd = lambda *s: torch.randint(0, 256, s, device="cuda", dtype=u8)
+for R, N, K in ((64, 264, 288), (1024, 264, 288), (4000, 2568, 2816)):
+    x, T, k = torch.randn(R, K, device="cuda").to(bf16), R // 2, 2
+    inv = torch.arange(R, device="cuda", dtype=torch.int32)
+    tw = torch.rand(T, k, device="cuda")
+    w = torch.zeros(moe.moe_mxfp4_weight_bytes(1, N, K), dtype=u8, device="cuda")
+    ws = torch.zeros(moe.moe_mxfp4_weight_scale_bytes(1, N, K), dtype=u8, device="cuda")
+    raw, raw_s = rnd(1, N, K // 2), torch.full((1, N, K // 32), 127, dtype=u8, device="cuda")
+    codes = torch.zeros(R, K // 2, dtype=u8, device="cuda")
+    scales = torch.zeros(moe.mxfp4_scale_shape(R, K, "group"), dtype=u8, device="cuda")
+    space = torch.zeros(moe.moe_mxfp4_workspace_bytes(R, 1, N, K), dtype=u8, device="cuda")
+    out, y = torch.zeros(R, N, dtype=bf16, device="cuda"), torch.zeros(T, N, dtype=bf16, device="cuda")
+    def step():
+        moe.moe_mxfp4_prepack(raw, raw_s, 1, N, K, w, ws)
+        moe.moe_quantize_mxfp4(x, "bf16", T, K, k, inv, codes, scales, "group")
+        moe.moe_mxfp4_gemm(codes, scales, None, R, 1, N, K, w, ws, "bf16", out, space)
+        moe.moe_unpermute(out, "bf16", T, N, k, inv, tw, y)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    graph.replay()
+    got = [t.clone() for t in (codes, scales, w, ws, out, y)]
+    assert moe.moe_mxfp4_check_error(space) == 0 and got[-1].abs().sum() > 0
+    for t in (codes, scales, w, ws, out, y):
+        t.zero_()
+    step()
+    assert all(torch.equal(a, b) for a, b in zip(got, (codes, scales, w, ws, out, y)))
+print("captured ok")
+"""
+
+
+def test_first_calls_of_a_process_are_captured():
+    """Every launch's first use inside a capture (kernels are loaded and set up there)."""
+    ensure_built()
+    root = os.path.abspath(os.path.join(os.path.dirname(__file__), ".."))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS.format(root=root)], capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and r.stdout.strip().endswith("captured ok"), r.stdout + r.stderr
