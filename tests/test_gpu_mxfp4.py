@@ -785,3 +785,59 @@ def test_first_calls_of_a_process_are_captured():
     r = subprocess.run([sys.executable, "-c", FIRST_CALLS.format(root=root)], capture_output=True, text=True,
                        timeout=300)
     assert r.returncode == 0 and r.stdout.strip().endswith("captured ok"), r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("T,H,N,k", [(1, 512, 264, 4), (37, 1024, 136, 2), (600, 288, 264, 3), (2000, 2816, 2568, 2)])
+def test_launches_that_overlap_read_what_the_last_one_wrote(T, H, N, k):
+    """Forty rounds on other tokens through the same buffers, captured without a gap: each
+    launch starts while those before it run, and rereads addresses that they rewrite."""
+    ensure_built()
+    g, n, S = _gen(T + H), 40, T * k
+    xs = torch.randn(n, T, H, generator=g, device="cuda").to(torch.bfloat16)
+    invs = [torch.randperm(S, generator=g, device="cuda").reshape(T, k).int() for _ in range(n)]
+    tw = [torch.rand(T, k, generator=g, device="cuda") for _ in range(n)]
+    p = Product(S, 1, N, H, *_operands(S, 1, N, H, 81))
+    rows, inv, w = torch.zeros(S, H, dtype=xs.dtype, device="cuda"), torch.empty_like(invs[0]), torch.empty_like(tw[0])
+    drows, y = torch.zeros_like(rows), torch.zeros(S, N, dtype=xs.dtype, device="cuda")
+
+    def make():
+        return [torch.zeros(n, T, H, dtype=xs.dtype, device="cuda"), torch.zeros(n, T, k, device="cuda"),
+                torch.zeros(n, T, H, dtype=xs.dtype, device="cuda"), torch.zeros(n, T, N, dtype=xs.dtype, device="cuda")]
+
+    def step(i, o, wait):
+        calls = (lambda: moe.moe_permute(invs[i], T, 4 * k, 1, first, inv),
+                 lambda: moe.moe_permute(tw[i], T, 4 * k, 1, first, w),
+                 lambda: moe.moe_permute(xs[i], T, H * 2, k, inv, rows),
+                 lambda: moe.moe_unpermute(rows, "bf16", T, H, k, inv, w, o[0][i]),
+                 lambda: moe.moe_unpermute_backward(xs[i], rows, "bf16", T, H, k, inv, w, drows, o[1][i]),
+                 lambda: moe.moe_permute_backward(drows, "bf16", T, H, k, inv, o[2][i]),
+                 lambda: moe.moe_quantize_mxfp4(xs[i], "bf16", T, H, k, inv, p.codes, p.scales, "group"),
+                 lambda: p(None, "bf16", y),
+                 lambda: moe.moe_unpermute(y, "bf16", T, N, k, inv, w, o[3][i]))
+        for call in calls:
+            call()
+            if wait:
+                torch.cuda.synchronize()
+
+    first = torch.arange(T, dtype=torch.int32, device="cuda")
+    want, got = make(), make()
+    for i in range(n):
+        step(i, want, True)
+    p.check()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for i in range(n):
+            step(i, got, False)
+    for _ in range(5):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    for t in got:
+        t.zero_()
+    for i in range(n):
+        step(i, got, False)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    p.check()
