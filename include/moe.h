@@ -343,8 +343,12 @@ typedef enum { MOE_SCALES_ROW_MAJOR = 0, MOE_SCALES_GROUP_MAJOR = 1 } moe_scale_
 /* Quantise x [T, K] of `dtype`.  Per 32 elements: n = the smallest integer
  * >= -127 with amax <= 6 * 2^n, scale byte n + 127, codes = E2M1 of x / 2^n,
  * round to nearest even.  (Unlike moe_quantize_act there is no floor under
- * amax: E2M1 spans a factor of 12, so a floor would flush small blocks.)  A
- * block with a NaN or an infinity gets scale byte 255 (NaN) and codes 0.
+ * amax: E2M1 spans a factor of 12, so a floor would flush small blocks.  And
+ * unlike the OCP microscaling specification's conversion, n = floor(log2 amax) - 2
+ * with values above 6 * 2^n cut to it, no value saturates: n is one higher where
+ * amax has a mantissa above 1.5.  Both are MXFP4; bytes compared with another
+ * quantiser's may differ there.)  A block with a NaN or an infinity gets scale
+ * byte 255 (NaN) and codes 0.
  * With inv (as for the row operators) the T tokens' rows are written once per
  * routed slot, straight into expert order: codes and scales have R = T*k rows,
  * and rows that no slot names are left as they were.  inv NULL (then k must be

@@ -415,7 +415,9 @@ def moe_forward_launch_count(plan):
 
 
 # The calls below run once per layer and token step, so their checks are written to
-# cost little: sizes in one expression, one call per buffer.
+# cost little: sizes in one expression, one call per buffer.  They write into the
+# tensors they are given and record nothing for autograd: the gradients are calls of
+# their own.
 
 
 def _sizes(fn, *values):

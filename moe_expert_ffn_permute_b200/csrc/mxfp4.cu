@@ -7,7 +7,9 @@
 //               (NaN) and codes 0: all its values are NaN.
 //   dequantise: value = E2M1 * 2^(byte - 127), exact in bf16 and fp32 (infinity
 //               from 2^128 on).
-//   prepack:    weights into the tiles and scale chunks the MXFP4 product reads.
+//   prepack:    weights into the tiles and scale chunks the MXFP4 product reads,
+//               once per weight set (32 x 4096 x 7168: 217 us for both launches,
+//               4.6 TB/s; the scales, read by bytes, take 59 of them).
 // The division by 2^n is exact, so the codes depend on the inputs alone.
 // HBM-bound: quantise reads an element once and writes 17/32 byte for it, once
 // per slot when it also copies the rows into expert order (8192 x 7168 bf16: in

@@ -26,10 +26,11 @@
 //
 // Few tokens: bound by the weight stream.  One token through 8 experts, 7168 ->
 // 4096, 23.8 us (125 MB, 5.2 TB/s; 1.8 us until the first weights, 1.5 us from the
-// last MMA to the next kernel); a skewed batch of 128 tokens, 28 of 32 experts, 75 us
-// (449 MB, 6.0 TB/s), 70 without its MMAs.  Many tokens: operand delivery into
-// shared memory (52 KB per SM and K block) and then the power cap; mxfp4_pair.cu
-// takes those.
+// last MMA to the next kernel), 2048 -> 7168 15.9 us (63 MB in four rounds of tiles);
+// a skewed batch of 128 tokens, 28 of 32 experts, 75 to 78 us (449 MB, 5.9 TB/s), 70
+// without its MMAs, and 42 us 2048 -> 7168 (39 without its stores).  Many tokens:
+// operand delivery into shared memory (52 KB per SM and K block) and then the power
+// cap; mxfp4_pair.cu takes those.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -55,9 +56,10 @@ constexpr uint32_t kTmemCols = 512;
 // TMEM: the accumulator takes columns 0..255; two scale sets, used in turn so
 // that a copy never lands in the set that MMAs just issued may still read.  A
 // set holds 2 x 4 columns of weight scales and 2 x 8 of token scales (rows
-// 0..127 and 128..255 of the tile, for each half of the stage's K).  (Two
-// accumulators of 224 columns used in turn measured the same at equal tiles, and
-// the smaller tiles cost 10%: the epilogue frees TMEM as soon as it has loaded.)
+// 0..127 and 128..255 of the tile, for each half of the stage's K).  (With tiles of
+// 128 tokens two accumulators used in turn measured the same as one, on decode
+// batches and groups of 32 to 144 rows: the epilogue frees TMEM as soon as it has
+// loaded.  Not measured on large tiles of short K.)
 constexpr uint32_t kSfCol = 256, kSfSet = 32, kSfTokens = 8;
 
 // kTok: most tokens of a tile.  256: the fewest weight reads per token; 128: half

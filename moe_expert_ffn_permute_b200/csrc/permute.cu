@@ -291,7 +291,9 @@ moe_status moe_permute(const void* x, int T, int64_t row_bytes, int k, const int
     return MOE_ERR_ALIGNMENT;
   auto st = reinterpret_cast<cudaStream_t>(stream);
   // Rows of whole 16-byte vectors keep every row 16-byte aligned; others
-  // (scale bytes of odd sizes) go word by word.
+  // (scale bytes of odd sizes) go word by word, at about half the rate (65536
+  // tokens, top-8: rows of 1792 bytes 189 us, of 1796 bytes 358; 224 and 228
+  // bytes 28 and 58).
   const bool wide = row_bytes % 16 == 0;
   const long long vecs = row_bytes / (wide ? 16 : 4);
   const unsigned blocks = moe::copy_blocks(T, vecs, k);
