@@ -1,5 +1,6 @@
 // api.cu -- the C ABI (include/moe.h): plan construction and validation,
 // workspace layout, and the stream-ordered launch sequence of the layer.
+#include <atomic>
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -45,6 +46,20 @@ cudaError_t ensure_max_dynamic_smem(const void* kernel, int bytes) {
     return cudaErrorMemoryAllocation;
   }
   return e;
+}
+
+EncodeTiledFn tensor_map_encoder() {
+  static std::atomic<EncodeTiledFn> found{nullptr};
+  EncodeTiledFn fn = found.load(std::memory_order_relaxed);
+  if (fn != nullptr) return fn;
+  void* ptr = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) ==
+          cudaSuccess &&
+      q == cudaDriverEntryPointSuccess)
+    fn = reinterpret_cast<EncodeTiledFn>(ptr);
+  found.store(fn, std::memory_order_relaxed);   // (a failure is looked up again)
+  return fn;
 }
 
 static size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }

@@ -122,6 +122,13 @@ int sm_count();
 // device, once per (kernel, device); thread-safe.
 cudaError_t ensure_max_dynamic_smem(const void* kernel, int bytes);
 
+// The driver's cuTensorMapEncodeTiled (nullptr without a driver that has it).
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn tensor_map_encoder();
+
 // Sizes the MXFP4 product and its weight layout take: whole 32-wide blocks of K,
 // output rows of whole 16-byte vectors, and tile counts that fit their types.
 constexpr int kMxMaxExperts = 256;

@@ -335,23 +335,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 // --------------------------------------------------------------- host side
 thread_local int g_debug_fault = 0;   // moe_mxfp4_set_debug
 
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static const EncodeTiledFn fn = [] {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    const bool ok = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault,
-                                            &q) == cudaSuccess &&
-                    q == cudaDriverEntryPointSuccess;
-    return ok ? reinterpret_cast<EncodeTiledFn>(ptr) : nullptr;
-  }();
-  return fn;
-}
-
 template <int kTok, bool kFp16>
 cudaError_t launch(const MxGemm& p, cudaStream_t st) {
   CUtensorMap map;
@@ -422,7 +405,7 @@ bool use_pairs(int R, int E, int N, int K) {
 
 bool mx::map_rows(CUtensorMap* m, const void* base, uint64_t width, uint64_t rows, uint32_t box,
                   uint32_t box_rows, bool swizzle128) {
-  const EncodeTiledFn enc = encode_fn();
+  const EncodeTiledFn enc = tensor_map_encoder();
   if (enc == nullptr) return false;
   std::memset(m, 0, sizeof(*m));
   const cuuint64_t dims[2] = {width, rows};
