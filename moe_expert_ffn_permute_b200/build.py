@@ -12,7 +12,7 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "libmoe_b200.so")
 SOURCES = ["api.cu", "route.cu", "gemm.cu", "combine.cu", "quant.cu", "layout.cu", "gemm2.cu",
            "permute.cu", "mxfp4.cu", "mxfp4_gemm.cu", "mxfp4_pair.cu"]
-HEADERS = ["internal.h", "sm100.cuh", "sm100_pair.cuh", "elem.cuh", "mxfp4_tiles.cuh"]
+HEADERS = ["internal.h", "sm100.cuh", "sm100_pair.cuh", "elem.cuh", "args.h", "mxfp4_tiles.cuh"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
          "-Xcompiler", "-fPIC", "-shared", "-cudart", "static", "--expt-relaxed-constexpr"]

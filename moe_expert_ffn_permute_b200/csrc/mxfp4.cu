@@ -19,6 +19,7 @@
 // accesses each touch half of their sectors.
 #include <cuda_runtime.h>
 
+#include "args.h"
 #include "elem.cuh"
 #include "internal.h"
 #include "sm100.cuh"

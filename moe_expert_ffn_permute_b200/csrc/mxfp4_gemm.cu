@@ -37,7 +37,7 @@
 #include <algorithm>
 #include <cstring>
 
-#include "elem.cuh"
+#include "args.h"
 #include "internal.h"
 #include "mxfp4_tiles.cuh"
 #include "sm100.cuh"

@@ -24,7 +24,6 @@
 #include <algorithm>
 #include <cstring>
 
-#include "elem.cuh"
 #include "internal.h"
 #include "mxfp4_tiles.cuh"
 #include "sm100_pair.cuh"

@@ -15,6 +15,7 @@
 
 #include <algorithm>
 
+#include "args.h"
 #include "elem.cuh"
 #include "internal.h"
 #include "sm100.cuh"
